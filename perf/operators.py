@@ -171,7 +171,7 @@ def _prepare_extend(case, gen, rnd):
         from fp4_kv_cache_quantize_b200 import csa2
         style = csa2.ROPE_HALVES if case["halves"] else csa2.ROPE_PAIRS
         kv = csa2.KVCache(s["codes"], s["scales"], s["idx_k"], s["n_rows"],
-                          max_rows=1 << 20, seq_stride=stride, page_table=page_table)
+                          max_rows=max(n + c for n, c in zip(n0, counts)), seq_stride=stride, page_table=page_table)
         rope = csa2.Rope(s["table"], style)
         rope_idx = csa2.Rope(s["table_idx"], style) if case["idx_dims"] else None
         more = dict(x_swa=s["x_swa"], swa=s["swa"], swa_pos=s["swa_pos"], swa_len=s["swa_len"], rope_swa=rope) if L else {}
