@@ -19,6 +19,8 @@ D, H, HI, DI, BLK, W = 512, 16, 8, 64, 8, 128
 MAX_TOPK, MAX_POOL, MAX_ROWS = 512, 2048, 1 << 20
 WS_HEADER = 256
 FULL, REINDEX, REUSE = 0, 1, 2
+ROPE_PAIRS, ROPE_HALVES = 0, 1
+PREFIX_MAX_BATCH = 1024
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_SHAPE",
           3: "CSA2_ERR_ALIGNMENT", 4: "CSA2_ERR_WORKSPACE", 5: "CSA2_ERR_CUDA",
@@ -51,6 +53,25 @@ class GroupDesc(C.Structure):
                 ("pool_blocks", C.c_int32), ("sm_scale", C.c_float), ("idx", C.c_void_p),
                 ("idx_count", C.c_void_p), ("pool", C.c_void_p), ("pool_count", C.c_void_p),
                 ("out", C.c_void_p), ("n_query", C.c_int32)]
+
+
+class RopeStruct(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("n_pos", C.c_int32), ("dims", C.c_int32),
+                ("style", C.c_int32)]
+
+
+class ExtendDesc(C.Structure):
+    _fields_ = [("kv", KVView), ("total", C.c_int32), ("cu_tokens", C.c_void_p),
+                ("pos", C.c_void_p), ("x", C.c_void_p), ("w_idx", C.c_void_p),
+                ("rope", RopeStruct), ("rope_idx", RopeStruct), ("rope_swa", RopeStruct),
+                ("n_layers", C.c_int32), ("x_swa", C.c_void_p), ("swa", C.c_void_p),
+                ("swa_pos", C.c_void_p), ("swa_len", C.c_void_p)]
+
+
+class PrefixDesc(C.Structure):
+    _fields_ = [("kv", KVView), ("prefix_rows", C.c_int32), ("n_query", C.c_int32),
+                ("q", C.c_void_p), ("swa", C.c_void_p), ("swa_len", C.c_void_p),
+                ("sm_scale", C.c_float), ("out", C.c_void_p)]
 
 
 class TraceStruct(C.Structure):
@@ -96,6 +117,12 @@ _selftest_wait = _sig("csa2_selftest_bounded_wait", C.c_int, [_vp, _sz, _i64, _v
 _trace_set = _sig("csa2_trace_set", None, [_vp])
 _group_ws = _sig("csa2_group_workspace_size", _sz, [C.POINTER(GroupDesc)])
 _group = _sig("csa2_layer_group", C.c_int, [C.POINTER(GroupDesc), _vp, _sz, _vp])
+
+_rope_rows = _sig("csa2_rope_rows", C.c_int,
+                  [C.POINTER(RopeStruct), _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _sz, _vp])
+_extend = _sig("csa2_cache_extend", C.c_int, [C.POINTER(ExtendDesc), _vp, _sz, _vp])
+_prefix_ws = _sig("csa2_prefix_attn_workspace_size", _sz, [C.POINTER(PrefixDesc)])
+_prefix = _sig("csa2_prefix_attn", C.c_int, [C.POINTER(PrefixDesc), _vp, _sz, _vp])
 
 
 class CpShard(C.Structure):
@@ -298,6 +325,125 @@ def csa2_group_workspace_size(group: LayerGroup) -> int:
 
 def csa2_layer_group(group: LayerGroup, ws, stream=None):
     _check(_group(C.byref(group.desc), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ------------------------------------- rotation, cache extension, shared prefix
+def _typed(t, dtypes, shape, what):
+    """The argument's dtype and shape, as its C entry point will read it."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    return t
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_INT = (torch.int32,)
+
+
+class Rope:
+    """A csa2_rope over table fp32 [n_pos][dims / 2][2] of (cos, sin), kept
+    alive by this object; style ROPE_PAIRS or ROPE_HALVES."""
+
+    def __init__(self, table, style: int = ROPE_PAIRS):
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError("table must be [n_pos][dims / 2][2]")
+        self.table = _typed(table, (torch.float32,), None, "table")
+        self.s = RopeStruct(_ptr(table), int(table.shape[0]), 2 * int(table.shape[1]), int(style))
+
+
+def csa2_rope_rows(rope: Rope, x, pos, y, ws, inverse: bool = False, stream=None):
+    """y[r][h] = x[r][h] rotated by pos[r] (back, if inverse): x, y bf16
+    [rows][heads][ch], pos int32 [rows]; y may be x."""
+    rows, heads, ch = _typed(x, _BF16, None, "x").shape
+    _typed(y, _BF16, x.shape, "y")
+    _typed(pos, _INT, (rows,), "pos")
+    _check(_rope_rows(C.byref(rope.s), _ptr(x), _ptr(pos), rows, heads, ch, int(bool(inverse)),
+                      _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+class CacheExtend:
+    """A csa2_extend_desc over device tensors (kept alive by this object):
+    x bf16 [total][512] appended to kv's sequences (cu_tokens int32
+    [batch + 1]; None: one token each) and x_swa bf16 [L][total][512] to the
+    window rings swa E4M3 [L][batch][128][512], rotated by pos int32 [total]
+    (None: the cache position).  See csa2.h."""
+
+    def __init__(self, kv: KVCache, x=None, w_idx=None, *, cu_tokens=None, pos=None, rope=None,
+                 rope_idx=None, rope_swa=None, x_swa=None, swa=None, swa_pos=None, swa_len=None):
+        if x is None and x_swa is None:
+            raise ValueError("x or x_swa is required")
+        total = int(x.shape[0]) if x is not None else int(x_swa.shape[1])
+        L = 0 if x_swa is None else int(x_swa.shape[0])
+        if x is not None:
+            _typed(x, _BF16, (total, D), "x")
+            if w_idx is None:
+                raise ValueError("w_idx is required with x")
+            _typed(w_idx, _BF16, (D, DI), "w_idx")
+        if cu_tokens is not None:
+            _typed(cu_tokens, _INT, (kv.batch + 1,), "cu_tokens")
+        if pos is not None:
+            _typed(pos, _INT, (total,), "pos")
+        if L:
+            if swa is None or swa_pos is None or swa_len is None:
+                raise ValueError("swa, swa_pos and swa_len are required with x_swa")
+            _typed(x_swa, _BF16, (L, total, D), "x_swa")
+            _typed(swa, _E4M3, (L, kv.batch, W, D), "swa")
+            _typed(swa_pos, _INT, (kv.batch,), "swa_pos")
+            _typed(swa_len, _INT, (kv.batch,), "swa_len")
+        self.keep = (kv, x, w_idx, cu_tokens, pos, rope, rope_idx, rope_swa, x_swa, swa, swa_pos,
+                     swa_len)
+        none = RopeStruct(None, 0, 0, 0)
+        ropes = [none if r is None else r.s for r in (rope, rope_idx, rope_swa)]
+        self.desc = ExtendDesc(kv.view, total, _ptr(cu_tokens), _ptr(pos), _ptr(x), _ptr(w_idx),
+                               *ropes, L, _ptr(x_swa), _ptr(swa), _ptr(swa_pos), _ptr(swa_len))
+
+
+def csa2_cache_extend(ext: CacheExtend, ws, stream=None):
+    _check(_extend(C.byref(ext.desc), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+class PrefixAttn:
+    """A csa2_prefix_desc over device tensors (kept alive by this object):
+    dense attention of q bf16 [batch * n_query][16][512] over kv, the first
+    prefix_rows positions shared (sequence 0's rows), plus the window swa E4M3
+    [batch][128 + n_query - 1][512] with swa_len int32 [batch] (None: no
+    window).  See csa2.h."""
+
+    def __init__(self, kv: KVCache, q, prefix_rows: int, *, swa=None, swa_len=None, sm_scale=None,
+                 out=None, n_query: int = 1):
+        nq = int(n_query)
+        n = kv.batch * max(nq, 1)
+        if q.numel() != n * H * D:
+            raise ValueError(f"q has {q.numel()} values, not {n} x {H} x {D}")
+        self.q = _typed(q, _BF16, None, "q")
+        if (swa is None) != (swa_len is None):
+            raise ValueError("swa and swa_len go together")
+        if swa is not None:
+            _typed(swa, _E4M3, (kv.batch, W + max(nq, 1) - 1, D), "swa")
+            _typed(swa_len, _INT, (kv.batch,), "swa_len")
+        self.kv, self.swa, self.swa_len = kv, swa, swa_len
+        self.out = out if out is not None else torch.empty((n, H, D), dtype=torch.bfloat16,
+                                                           device=q.device)
+        if self.out.numel() != n * H * D:
+            raise ValueError(f"out has {self.out.numel()} values, not {n} x {H} x {D}")
+        _typed(self.out, _BF16, None, "out")
+        if sm_scale is None:
+            sm_scale = D ** -0.5
+        self.desc = PrefixDesc(kv.view, int(prefix_rows), nq, _ptr(q), _ptr(swa), _ptr(swa_len),
+                               float(sm_scale), _ptr(self.out))
+
+    def workspace_size(self) -> int:
+        return _prefix_ws(C.byref(self.desc))
+
+
+def csa2_prefix_attn_workspace_size(attn: PrefixAttn) -> int:
+    return attn.workspace_size()
+
+
+def csa2_prefix_attn(attn: PrefixAttn, ws, stream=None):
+    _check(_prefix(C.byref(attn.desc), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 class Trace:

@@ -163,6 +163,75 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
 
+// ------------------------------------------------ rotation, cache extension
+struct RopeParams {
+  const float2* table;  // [n_pos][dims / 2] (cos, sin); NULL: no rotation
+  int32_t n_pos, dims, style;
+};
+struct RopeRowsParams {
+  RopeParams rope;
+  const uint16_t* x;
+  uint16_t* y;
+  const int32_t* pos;
+  int64_t rows;
+  int32_t heads, ch;
+  int32_t inverse, in_place;
+  uint32_t* status;
+};
+cudaError_t launch_rope_rows(const RopeRowsParams& p, cudaStream_t st);
+
+struct ExtendParams {
+  uint8_t* codes;
+  uint8_t* scales;
+  uint16_t* idx_k;
+  const int32_t* page_table;
+  int32_t max_pages;
+  int64_t seq_stride;
+  int64_t pool_rows;
+  int32_t* n_rows;
+  int32_t batch;
+  int32_t total;
+  const int32_t* cu;      // [batch + 1] or NULL: one token each
+  const int32_t* pos;     // [total] or NULL: the cache / window position
+  const uint16_t* x;      // [total][512] or NULL: windows only
+  const uint16_t* w_idx;  // [512][64]
+  RopeParams rope, rope_idx, rope_swa;
+  int32_t n_layers;
+  const uint16_t* x_swa;  // [n_layers][total][512]
+  uint8_t* swa;           // [n_layers][batch][128][512] or NULL
+  int32_t* swa_pos;
+  int32_t* swa_len;
+  uint32_t* status;
+};
+cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st);
+
+// prefix_attn.cu -------------------------------------------------------
+struct PrefixParams {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const int32_t* page_table;
+  int32_t max_pages;
+  int32_t max_rows;
+  int64_t seq_stride;
+  int64_t pool_rows;
+  const int32_t* n_rows;
+  int32_t batch, nq, prefix;
+  const uint16_t* q;
+  const uint8_t* swa;       // NULL: no window
+  const int32_t* swa_len;
+  int32_t swa_rows;         // 128 + nq - 1
+  float scale_log2;
+  uint16_t* out;
+  float* part_o;    // partials of the shared tiles, then of the own tiles
+  float* part_ml;   // (max, sum) per row, laid out alike
+  int32_t grid;     // CTAs that the work is cut for
+  uint32_t* status;
+};
+// CTAs to launch, and the workspace for their partials, from host bounds.
+int prefix_grid(const PrefixParams& p, int num_sms);
+size_t prefix_partial_rows(const PrefixParams& p);
+cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t st);
+
 // ------------------------------------------------- context-parallel decode
 constexpr int CP_MAX_PARTS = 16;  // shards (and attention splits) one merge combines
 constexpr int CP_MAX_LISTS = AT_MAX_LAYERS;  // lists one filter launch handles

@@ -1,0 +1,87 @@
+// prefix_plan.cuh -- how csa2_prefix_attn cuts its work, the same arithmetic
+// for the kernel that computes the partials and the one that merges them.
+//
+// A tile is 128 keys against up to 64 query rows (a row is one head of one
+// query).  A segment is every key tile of one row block: first the blocks of 64
+// rows of the whole batch against the shared prefix, then, per sequence, its
+// blocks of up to four queries against its own rows and its window.  The tiles
+// lie on one line in segment order, each as long as it costs, and CTA i of G
+// takes the tiles that start in [i C / G, (i + 1) C / G): every CTA gets an
+// equal share whatever the lengths, and one partial per segment that it touches.
+// (segment + CTA) rises along the line, so it numbers the partials.
+#pragma once
+
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace csa2 {
+
+constexpr int PA_KEYS = 128;     // keys per tile: the MMA's M
+constexpr int PA_ROWS = 64;      // query rows per tile: the MMA's N
+constexpr int PA_QB = PA_ROWS / CSA2_H;  // queries per row block
+constexpr int PA_MAX_GRID = 192;
+
+// What a tile of n rows costs, relative to others.
+__host__ __device__ inline int pa_cost(int n_rows) { return 12 + n_rows / 16; }
+
+struct PaPlan {
+  int row_blocks;   // blocks of 64 rows over the whole batch
+  int prefix_tiles; // key tiles of the shared prefix
+  int q_blocks;     // row blocks per sequence for its own rows
+  int own_rows;     // rows of a partial of an own segment
+  int win_tiles;    // window tiles per own segment
+  int shared;       // tiles of the shared segments
+  int cost_p, cost_o;
+  int64_t base, total;  // costs of the shared tiles, and of all
+  int grid;
+
+  // own: key tiles of all sequences' own rows and windows, per row block
+  __host__ __device__ void finish(int64_t own) {
+    base = (int64_t)shared * cost_p;
+    total = base + own * q_blocks * cost_o;
+  }
+  __host__ __device__ int64_t tile_at(int i) const {  // first tile of CTA i
+    const int64_t x = total * i / grid;
+    if (x <= base) return (x + cost_p - 1) / cost_p;
+    return shared + (x - base + cost_o - 1) / cost_o;
+  }
+  __host__ __device__ int64_t cost_before(int64_t tile) const {
+    return tile < shared ? tile * cost_p : base + (tile - shared) * cost_o;
+  }
+  __host__ __device__ int cta_of(int64_t tile) const {
+    return (int)(((cost_before(tile) + 1) * grid - 1) / total);
+  }
+  // first row of the partial of CTA c for a shared / an own segment
+  __host__ __device__ int64_t shared_slot(int seg, int c) const {
+    return (int64_t)(seg + c) * PA_ROWS;
+  }
+  __host__ __device__ int64_t own_slot(int seg, int c) const {
+    return (int64_t)(row_blocks + grid) * PA_ROWS + (int64_t)(seg + c) * own_rows;
+  }
+};
+
+__host__ __device__ inline PaPlan pa_plan(const PrefixParams& p) {
+  PaPlan pl;
+  const int rows = p.batch * p.nq * CSA2_H;
+  pl.row_blocks = (rows + PA_ROWS - 1) / PA_ROWS;
+  pl.prefix_tiles = (p.prefix + PA_KEYS - 1) / PA_KEYS;
+  pl.q_blocks = (p.nq + PA_QB - 1) / PA_QB;
+  pl.own_rows = CSA2_H * (p.nq < PA_QB ? p.nq : PA_QB);
+  // the windows of a block of k queries span 128 + k - 1 rows
+  pl.win_tiles = p.swa == nullptr ? 0 : (p.nq == 1 ? 1 : 2);
+  pl.shared = pl.row_blocks * pl.prefix_tiles;
+  pl.cost_p = pa_cost(rows < PA_ROWS ? rows : PA_ROWS);
+  pl.cost_o = pa_cost(pl.own_rows);
+  pl.base = pl.total = 0;
+  pl.grid = p.grid;
+  return pl;
+}
+
+// Key tiles of sequence b's own rows (beyond the prefix), without its window.
+__host__ __device__ inline int pa_own_tiles(const PrefixParams& p, int n_rows) {
+  const int n = n_rows < 0 ? 0 : (n_rows > p.max_rows ? p.max_rows : n_rows);
+  return n > p.prefix ? (n - p.prefix + PA_KEYS - 1) / PA_KEYS : 0;
+}
+
+}  // namespace csa2

@@ -360,6 +360,156 @@ size_t csa2_group_workspace_size(const csa2_group_desc *desc);
 csa2_status csa2_layer_group(const csa2_group_desc *desc, void *ws, size_t ws_bytes,
                              csa2_stream_t stream);
 
+/* ------------------------------------------------------ position rotation */
+
+/*
+ * Rotary positions.  A row whose last `dims` channels are rotated by position
+ * n has each pair (a, b) of them replaced by
+ *   a' = a cos - b sin,   b' = a sin + b cos,
+ * (cos, sin) = table[n][i] for pair i < dims / 2.  CSA2_ROPE_PAIRS pairs the
+ * rotated channels (2i, 2i + 1), CSA2_ROPE_HALVES (i, i + dims / 2).  Both
+ * sums are formed in fp64 (the products of a bf16 and an fp32 value are exact
+ * there) and rounded to fp32 and then to bf16, nearest even: results do not
+ * depend on which call rotates.  The table is the caller's, so any frequency
+ * schedule and any scaling of it is the caller's too.
+ *   table  device fp32 [n_pos][dims / 2][2], 16-byte aligned; NULL in a
+ *          descriptor below means no rotation (the other members are ignored)
+ *   n_pos  positions in the table, >= 1.  A position outside [0, n_pos) is
+ *          clamped and recorded as CSA2_ERR_DEVICE_CHECK.
+ *   dims   rotated channels, a multiple of 32, at most the row's channels
+ */
+enum { CSA2_ROPE_PAIRS = 0, CSA2_ROPE_HALVES = 1 };
+
+typedef struct {
+  const float *table;
+  int32_t n_pos;
+  int32_t dims;
+  int32_t style; /* CSA2_ROPE_PAIRS or CSA2_ROPE_HALVES */
+} csa2_rope;
+
+/*
+ * Rotate rows by position: y[r][h][:] = the rotation of x[r][h][:] by pos[r]
+ * (inverse != 0: by -pos[r]).  For the queries that meet keys rotated by
+ * csa2_cache_extend, and, because a main-KV row is key and value at once, for
+ * turning attention outputs back by the query's position.
+ *   x, y   bf16 [rows][heads][ch]; y == x rotates in place (then only the
+ *          rotated channels are touched); otherwise they must not overlap.
+ *   pos    int32 [rows], 4-byte aligned;  ch a multiple of 8, ch <= 65536;
+ *          rows, heads >= 0 with rows * heads * ch < 2^40; 0 rows do nothing.
+ *   ws     a workspace of at least CSA2_WS_HEADER bytes (status word).
+ */
+csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32_t *pos,
+                           int64_t rows, int32_t heads, int32_t ch, int32_t inverse, uint16_t *y,
+                           void *ws, size_t ws_bytes, csa2_stream_t stream);
+
+/* --------------------------------------------------------- cache extension */
+
+/*
+ * Append a run of entries to every sequence, rotated by position on the way:
+ * prompt chunks, draft positions, or one entry each.  Tokens
+ * cu_tokens[b] .. cu_tokens[b + 1) of x belong to sequence b; token i of its
+ * run (count of them) goes to position p = kv.n_rows[b] + i:
+ *   codes/scales row of p  <- FP4 of R(x) (as csa2_quantize_fp4 of the bf16
+ *                             row that csa2_rope_rows gives),
+ *   idx_k row of p         <- bf16_rne(R_idx(x @ w_idx))  (the entry as
+ *                             produced, fp32 accumulation, rotated before its
+ *                             one rounding),
+ *   for each layer l < n_layers: slot (swa_pos[b] + i) % 128 of
+ *   swa[l][b]              <- E4M3 (nearest even, saturating to +-448) of the
+ *                             bf16 row R_swa(x_swa[l][token]); of a run longer
+ *                             than 128 only the last 128 are written,
+ * then kv.n_rows[b] and swa_pos[b] advance by count and swa_len[b] becomes
+ * min(swa_pos[b], 128).  Rows behind the run keep what they held.
+ * Members (device memory, caller-owned, 16-byte aligned unless noted):
+ *   kv         the cache, written as by csa2_cache_append.  kv.max_rows is not
+ *              checked against the new positions.
+ *   total      tokens in x (host), 0 <= total < 2^24 (0 does nothing); tokens at
+ *              or past cu_tokens[batch] are ignored (a padded batch)
+ *   cu_tokens  int32 [batch + 1] non-decreasing from 0, 4-byte aligned; NULL:
+ *              one token each (then total must equal kv.batch)
+ *   pos        int32 [total] rotation positions, 4-byte aligned; NULL: p for
+ *              the entry and its key, swa_pos[b] + i for the window entries
+ *   x          bf16 [total][512], w_idx bf16 [512][64]; x NULL: windows only
+ *              (of kv only the batch is used then)
+ *   rope, rope_idx, rope_swa  rotations of the entry, of its indexer key
+ *              (dims <= 64) and of the window entries
+ *   n_layers   0: no windows; x_swa bf16 [n_layers][total][512],
+ *              swa E4M3 [n_layers][batch][128][512], swa_pos and swa_len int32
+ *              [batch] (4-byte aligned)
+ * A sequence whose run does not fit (a position beyond its capacity or on an
+ * unmapped page, a negative counter, token offsets out of order or beyond
+ * total) is left unchanged as a whole, rows, windows and counters, and
+ * CSA2_ERR_DEVICE_CHECK is recorded.  ws: at least CSA2_WS_HEADER bytes.
+ * Two launches; asynchronous on stream.
+ */
+typedef struct {
+  csa2_kv_view kv;
+  int32_t total;
+  const int32_t *cu_tokens;
+  const int32_t *pos;
+  const uint16_t *x;
+  const uint16_t *w_idx;
+  csa2_rope rope;
+  csa2_rope rope_idx;
+  csa2_rope rope_swa;
+  int32_t n_layers;
+  const uint16_t *x_swa;
+  uint8_t *swa;
+  int32_t *swa_pos;
+  int32_t *swa_len;
+} csa2_extend_desc;
+
+csa2_status csa2_cache_extend(const csa2_extend_desc *desc, void *ws, size_t ws_bytes,
+                              csa2_stream_t stream);
+
+/* ------------------------------------------- attention over a shared prefix */
+
+/*
+ * Dense decode attention of one layer for a batch whose sequences share their
+ * first prefix_rows positions: csa2_sparse_attn_decode with every visible row
+ * selected, the prefix read, dequantised and multiplied once for all
+ * sequences' queries.  For query t < n_query of sequence b and head h,
+ *   keys = values = [ dequant(main KV at positions p < e) ;
+ *                     E4M3 window rows [max(0, f - 128), f) ],
+ *   e = kv.n_rows[b] - (n_query - 1 - t),  f = swa_len[b] - (n_query - 1 - t),
+ *   out = softmax_j(sm_scale * q . key_j) . values   (no keys gives zeros).
+ * Positions p < prefix_rows are read from SEQUENCE 0's rows for every
+ * sequence (paged: its page table; contiguous: its rows; a sequence shorter
+ * than the prefix sees the rows below its own e), the others from the
+ * sequence's own.  prefix_rows = 0 is dense attention without sharing.
+ * Members (device memory, 16-byte aligned unless noted):
+ *   kv           idx_k is not read and may be NULL; n_rows 4-byte aligned;
+ *                kv.batch <= CSA2_PREFIX_MAX_BATCH
+ *   prefix_rows  in [0, kv.max_rows] (host)
+ *   n_query      queries per sequence, in [1, CSA2_MAX_QUERY], their entries
+ *                already in the caches; kv.batch * n_query <= 65535
+ *   q, out       bf16 [batch][n_query][16][512] (any finite q)
+ *   swa          E4M3 [batch][128 + n_query - 1][512], rows in order, with
+ *                swa_len int32 [batch] <= 128 + n_query - 1 (4-byte aligned);
+ *                NULL (both): no window
+ * Rows that the page table maps outside the pool are skipped and recorded as
+ * CSA2_ERR_DEVICE_CHECK, and so is a count outside its range (clamped).
+ * Results do not depend on timing: every sum has a fixed order.
+ * Two launches; asynchronous on stream.
+ */
+enum { CSA2_PREFIX_MAX_BATCH = 1024 };
+
+typedef struct {
+  csa2_kv_view kv;
+  int32_t prefix_rows;
+  int32_t n_query; /* 0 or 1 = one */
+  const uint16_t *q;
+  const uint8_t *swa;
+  const int32_t *swa_len;
+  float sm_scale;
+  uint16_t *out;
+} csa2_prefix_desc;
+
+/* Workspace bytes of csa2_prefix_attn; 0 on a bad argument. */
+size_t csa2_prefix_attn_workspace_size(const csa2_prefix_desc *desc);
+csa2_status csa2_prefix_attn(const csa2_prefix_desc *desc, void *ws, size_t ws_bytes,
+                             csa2_stream_t stream);
+
 /* ------------------------------------------------ context-parallel decode */
 
 /*
