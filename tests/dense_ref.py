@@ -73,14 +73,20 @@ class Attention:
                 self.out[b, t] = w @ keys
                 # a logit is off by the fp32 sum of 512 products and the fp32
                 # roundings around it (8 units of its own size), and a weight
-                # by e^(2 d) - 1 (numerator and normaliser), its fp16 rounding
-                # (2^-11 in each) and 2^-32 a key of the sum lost below fp16's
-                # range; the sums over the keys and partials round in fp32;
-                # the result rounds once to bf16 (half a step: 2^-8)
+                # by e^(2 d) - 1 (numerator and normaliser) and its fp16
+                # rounding (2^-11 in each); the sums over the keys and partials
+                # round in fp32; the result rounds once to bf16 (half a step:
+                # 2^-8).  Those are relative to the weight.  Below fp16's normal
+                # range the rounding is absolute: weights are held as 2^7 w / r
+                # with r at most the row's largest weight, in steps of 2^-24, so
+                # each is off by at most 2^-25 r / 2^7 <= 2^-32 max w, whatever
+                # its own size, and the sum over keys by 2^-32 max w sum |v|
+                # (and the normaliser by 2^-32 max w a key)
                 d = ((q[b, t].abs() @ keys.abs().T) * abs(sm_scale) * 520 * 2.0 ** -24
                      + x.abs() * 8 * 2.0 ** -24).amax(-1, keepdim=True)
                 rel = 2 * d + 2.0 ** -10 + len(keys) * (2.0 ** -32 + 2.0 ** -24) + 2.0 ** -16
-                self.tol[b, t] = rel * (w @ keys.abs()) + self.out[b, t].abs() * 2.0 ** -8
+                self.tol[b, t] = (rel * (w @ keys.abs()) + self.out[b, t].abs() * 2.0 ** -8
+                                  + 2.0 ** -32 * w.amax(-1, keepdim=True) * keys.abs().sum(0))
         self.out, self.tol = self.out.view(B * nq, H, D), self.tol.view(B * nq, H, D)
 
     def check(self, got):
