@@ -11,12 +11,10 @@
 // O += p_j v_j, l += p_j.  m only has to be near the maximum: it is raised (and
 // O, l scaled) when some s_j exceeds it by 8, so p <= 2^15 fits fp16, and the
 // +7 keeps p to 2^-31 of the row's largest before it is lost: a million keys
-// lose at most 2^-12 of the sum together.  l sums the rounded p, so the weights
-// that multiply V are exactly normalised.
+// lose at most 2^-12 of the sum together.  (fp16 rounds each p by 2^-11 of
+// itself where bf16 would by 2^-8; l sums them unrounded, in fp32.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
-#include <cuda_fp8.h>
 
 #include "csa2_internal.cuh"
 #include "kernels.h"
@@ -24,30 +22,57 @@
 
 namespace csa2 {
 
-constexpr int PA_NT = 512;
-constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel block of the key tile
-constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel block of the queries
-constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), S^T behind
+// Roles of a CTA: eight warps turn key tiles into fp16, eight run the softmax,
+// one thread issues the MMAs.  Key tiles are 64 keys so that two fit next to the
+// queries: while one is multiplied, the next is written.  S^T then is an M = 64
+// product at half the tensor core's rate, but one that shared memory could not
+// feed faster anyway (4 KB of operands in 32 cycles); a single 128-key tile,
+// filled, multiplied and filled again, took twice as long.
+constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 8;
+constexpr int PA_MMA_WARP = PA_DQ_WARPS + PA_SM_WARPS;
+constexpr int PA_NT = 32 * (PA_MMA_WARP + 1);
+constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
+constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
+constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
 constexpr uint32_t PA_TMEM_COLS = 512;
 constexpr float PA_SHIFT = 7.0f, PA_SLACK = 8.0f;
 constexpr float PA_NONE = -1e30f;  // reference of a row that has met no key
 
+// One contiguous run of key tiles of one segment.
+struct PaRun {
+  int row0, n_rows;  // first query row of the batch, rows (a multiple of 16)
+  int seq;           // sequence whose row map is used
+  int kt, kt_end;    // key tiles (none if kt_end <= kt)
+  int line;          // how far the run goes on the line
+  int own_tiles;     // tiles at or past this are window tiles (own segments)
+  int first_pos;     // position of key 0 of tile 0
+  int n_keys;        // positions of the row map end here
+  int win_lo, n_win; // first window row of tile own_tiles, rows of the window
+  bool own;
+  bool valid;        // false: no run is left
+  int64_t slot;
+};
+
 struct PaSmem {
-  // K = V in fp16: channel block kb at kb * PA_KB, 128 rows (keys) of 128 B,
-  // 16-byte chunks swizzled by row % 8
-  alignas(1024) uint8_t tile[8 * PA_KB];
-  alignas(1024) uint8_t q[8 * PA_QKB];       // Q': block kb, 64 rows of 128 B
-  alignas(1024) uint8_t p[PA_KEYS * 128];    // P: [key][64 query rows] fp16
-  alignas(16) float scl1[PA_ROWS], scl2[PA_ROWS];  // logit = acc * scl1 * scl2 (log2 units)
-  alignas(16) float m[PA_ROWS];
-  alignas(16) int lo[PA_ROWS], hi[PA_ROWS];  // keys [lo, hi) are visible to the row
-  uint32_t bad[PA_KEYS];  // byte qq: quarter qq of the key row holds a NaN
+  // K = V in fp16, two tiles: channel chunk kb at kb * PA_KB, 64 rows (keys) of
+  // 128 B, 16-byte pieces swizzled by row % 8
+  alignas(1024) uint8_t tile[2][8 * PA_KB];
+  alignas(1024) uint8_t q[8 * PA_QKB];        // Q': chunk kb, 64 rows of 128 B
+  alignas(1024) uint8_t p[2][PA_KEYS * 128];  // P: [key][64 query rows] fp16
+  alignas(16) float scl[PA_ROWS];             // logit = acc * scl (log2 units)
+  alignas(16) float fac[PA_ROWS];             // what a raised reference scales O by
+  alignas(16) int lo[2][PA_ROWS], hi[2][PA_ROWS];  // cache, window: visible keys [lo, hi)
+  int lo_max[2], hi_min[2];                   // keys [lo_max, hi_min) are visible to all rows
+  // per tile: whether a key is missing (1) or holds a NaN (2), by quarter
+  alignas(16) uint8_t key[2][PA_KEYS][4];
   float red[4][PA_ROWS];
-  int cum[CSA2_PREFIX_MAX_BATCH + 1];        // own key tiles of sequences < b
-  int wsum[PA_NT / 32];
-  uint64_t mbar;
+  int cum[CSA2_PREFIX_MAX_BATCH + 1];         // own tiles on the line of sequences < b
+  int wsum[32];
+  uint64_t full[2], empty[2];    // tile buffer: written, multiplied
+  uint64_t s_full[2], p_full[2];
   uint32_t tmem_base;
   int abort;
+  PaRun run;
 };
 constexpr size_t PA_SMEM = sizeof(PaSmem) + 1024;
 static_assert(PA_SMEM <= 232448, "shared memory of one CTA");
@@ -64,153 +89,312 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+// Each thread of a warp reads 2 x 2 neighbours of every eight of 32 columns, of
+// 16 lanes.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
+}
+// Barrier of 128 threads that also tells whether any of them said so.
+__device__ __forceinline__ bool bar_or_128(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
 
-// One contiguous run of key tiles of one segment.
-struct PaRun {
-  int row0, n_rows;  // first query row of the batch, rows (a multiple of 16)
-  int seq;           // sequence whose row map is used
-  int kt, kt_end;    // key tiles
-  int own_tiles;     // tiles at or past this are window tiles (own segments)
-  int first_pos;     // position of key 0 of tile 0
-  int win_lo;        // first window row of tile own_tiles
-  bool own;
-  int64_t slot;
-};
-
-// This thread's quarter of one key row: raw bytes of key r, channels
-// [128 qq, 128 qq + 128).
-struct PaRaw {
-  uint4 v[8];
-  uint2 s;
-  bool ok;      // the key exists
-  bool window;  // E4M3 bytes, otherwise FP4 codes
-};
-
-__device__ __forceinline__ void pa_load(const PrefixParams& p, const PaRun& run, int kt, int r,
-                                        int qq, int n_own, int n_win, PaRaw& raw) {
-  raw.ok = false;
-  raw.window = run.own && kt >= run.own_tiles;
-  if (!raw.window) {
-    const int pos = run.first_pos + kt * PA_KEYS + r;
-    if (pos >= n_own) return;
-    int64_t row;
-    if (p.page_table) {
-      const int page = pos >> 6;
-      const int64_t pid =
-          page < p.max_pages ? (int64_t)__ldg(p.page_table + (int64_t)run.seq * p.max_pages + page)
-                             : -1;
-      row = pid < 0 ? -1 : pid * 64 + (pos & 63);
-    } else {
-      row = (int64_t)run.seq * p.seq_stride + pos;
-    }
-    if (row < 0 || row >= p.pool_rows) {
-      set_status(p.status, ST_DEVICE_CHECK);
-      return;
-    }
-    raw.ok = true;
-    const uint4* c = reinterpret_cast<const uint4*>(p.codes + row * (CSA2_D / 2) + 64 * qq);
-#pragma unroll
-    for (int i = 0; i < 4; i++) raw.v[i] = __ldg(c + i);
-    raw.s = __ldg(reinterpret_cast<const uint2*>(p.scales + row * (CSA2_D / 16) + 8 * qq));
+// Pool row of key r of tile kt, or -1: none (a mapping outside the pool is
+// recorded).
+__device__ __forceinline__ int64_t pa_row(const PrefixParams& p, const PaRun& run, int kt, int r) {
+  const int pos = run.first_pos + kt * PA_KEYS + r;
+  if (kt >= run.kt_end || (run.own && kt >= run.own_tiles) || pos >= run.n_keys) return -1;
+  int64_t row;
+  if (p.page_table) {
+    const int page = pos >> 6;
+    const int64_t pid =
+        page < p.max_pages ? (int64_t)__ldg(p.page_table + (int64_t)run.seq * p.max_pages + page)
+                           : -1;
+    row = pid < 0 ? -1 : pid * 64 + (pos & 63);
   } else {
-    const int j = run.win_lo + (kt - run.own_tiles) * PA_KEYS + r;
-    if (j >= n_win) return;
-    raw.ok = true;
-    const uint4* w = reinterpret_cast<const uint4*>(
-        p.swa + ((int64_t)run.seq * p.swa_rows + j) * CSA2_D + 128 * qq);
-#pragma unroll
-    for (int i = 0; i < 8; i++) raw.v[i] = __ldg(w + i);
+    row = (int64_t)run.seq * p.seq_stride + pos;
   }
+  if (row < 0 || row >= p.pool_rows) {
+    set_status(p.status, ST_DEVICE_CHECK);
+    return -1;
+  }
+  return row;
+}
+
+// Loads that stay where they are written: a plain read-only load may be moved
+// down to its use, one tile later, which put a whole memory latency in front of
+// every block.
+__device__ __forceinline__ uint4 ld_now_v4(const void* a) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_now_u16(const void* a) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(a));
+  return v;
 }
 
 // Whether a byte of w is an E4M3 NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool has_nan(uint32_t w) {
   return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
 }
-
-// A key that is not there, or whose values hold a NaN, becomes zeros: P = 0 of a
-// row that must not see it would otherwise turn NaN in the product.  Returns
-// whether it was a NaN: the rows that see the key then get NaN weights.
-__device__ __forceinline__ bool pa_dequant(const PaRaw& raw, uint8_t* tile, int r, int qq) {
-  uint8_t* trow = tile + r * 128;
-  const int sw = r & 7;
-  bool nan = false;
-  if (raw.ok && !raw.window) nan = has_nan(raw.s.x) || has_nan(raw.s.y);
-  if (raw.ok && raw.window) {
+// Two E4M3 bytes at bits 0 and 16 of w as fp16 times 2^-8: the four exponent
+// and three mantissa bits keep their places below the fp16 exponent's top bit,
+// which is right for E4M3's subnormals too.
+__device__ __forceinline__ __half2 e4m3x2_as_f16(uint32_t w) {
+  const uint32_t h = ((w & 0x007F007Fu) << 7) | ((w & 0x00800080u) << 8);
+  return *reinterpret_cast<const __half2*>(&h);
+}
+// Tile values are 2^-7 of the key's, so that the factor fits fp16 (below); the
+// logits' and the outputs' scales give it back.
+constexpr float PA_TILE_SCALE = 128.0f;
+// Eight FP4 codes (one word) times the scale f as fp16.  A code's bits s, eem go
+// to the fp16 sign and to bits 9..11, which reads as 2^-14 of the E2M1 value
+// (subnormal 0.5 included), by shifts and masks of two codes at once: the
+// conversion instruction has a small share of the ALU's rate (with it the
+// kernel spent 86% of its time in that unit).  f = scale * 2^7 <= 57,344 makes
+// the product value * scale * 2^-7: five significant bits above 2^-18, exact.
+// Codes j and j + 4 become neighbours; Q' has the same order and the outputs are
+// stored through pa_channel.
+__device__ __forceinline__ uint4 pa_fp4x8(uint32_t w, __half2 f) {
+  uint32_t h[4] = {((w << 12) & 0x80008000u) | ((w << 9) & 0x0E000E00u),
+                   ((w << 8) & 0x80008000u) | ((w << 5) & 0x0E000E00u),
+                   ((w << 4) & 0x80008000u) | ((w << 1) & 0x0E000E00u),
+                   (w & 0x80008000u) | ((w >> 3) & 0x0E000E00u)};
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-      nan |= has_nan(raw.v[j].x) || has_nan(raw.v[j].y) || has_nan(raw.v[j].z) ||
-             has_nan(raw.v[j].w);
+  for (int k = 0; k < 4; k++) h[k] = pa_h2u(__hmul2(*reinterpret_cast<__half2*>(&h[k]), f));
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+// Channel at place c of a tile row (within its group of eight).
+__device__ __forceinline__ int pa_channel(int c) {
+  return (c & ~7) | ((c & 7) >> 1) | ((c & 1) << 2);
+}
+// 32 FP4 codes (16 bytes) with their two E4M3 scales (low half of sc) into four
+// 16-byte pieces cc .. cc + 3 of a swizzled row.
+__device__ __forceinline__ void pa_put_fp4(uint8_t* row, int sw, int cc, uint4 v, uint32_t sc) {
+  const __half2 s2 = __hmul2(e4m3x2_as_f16((sc & 0xFFu) | ((sc & 0xFF00u) << 8)),
+                             __half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+  const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int c = 0; c < 4; c++)
+    *reinterpret_cast<uint4*>(row + (((cc + c) ^ sw) << 4)) =
+        pa_fp4x8(words[c], c < 2 ? __low2half2(s2) : __high2half2(s2));
+}
+// Eight E4M3 values (two words) as tile values.
+__device__ __forceinline__ uint4 pa_e4m3x8(uint32_t a, uint32_t b) {
+  const __half2 two = __half2(__ushort_as_half(0x4000), __ushort_as_half(0x4000));
+  uint32_t h[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const uint32_t w = ((a >> (8 * k)) & 0xFFu) | (((b >> (8 * k)) & 0xFFu) << 16);
+    h[k] = pa_h2u(__hmul2(e4m3x2_as_f16(w), two));
   }
-  if (!raw.ok || nan) {
-#pragma unroll
-    for (int j = 0; j < 16; j++)
-      *reinterpret_cast<uint4*>(trow + (2 * qq + (j >> 3)) * PA_KB + (((j & 7) ^ sw) << 4)) =
-          make_uint4(0, 0, 0, 0);
-  } else if (!raw.window) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {  // 16 code bytes: channels 128 qq + 32 i + [0, 32)
-      const uint32_t words[4] = {raw.v[i].x, raw.v[i].y, raw.v[i].z, raw.v[i].w};
-      const uint32_t sb = ((i < 2 ? raw.s.x : raw.s.y) >> (16 * (i & 1))) & 0xFFFFu;
-      const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sb, __NV_E4M3));
-      uint8_t* dst = trow + (2 * qq + (i >> 1)) * PA_KB;
-#pragma unroll
-      for (int c = 0; c < 4; c++) {  // 8 channels per 16-byte store
-        const __half2 s2 = c < 2 ? __low2half2(sc) : __high2half2(sc);
-        uint32_t hv[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-          hv[k] = pa_h2u(__hmul2(__half2(__nv_cvt_fp4x2_to_halfraw2(
-                                     (__nv_fp4x2_storage_t)((words[c] >> (8 * k)) & 0xFF),
-                                     __NV_E2M1)),
-                                 s2));
-        *reinterpret_cast<uint4*>(dst + (((4 * (i & 1) + c) ^ sw) << 4)) =
-            make_uint4(hv[0], hv[1], hv[2], hv[3]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++) {  // 16 E4M3 bytes: channels 128 qq + 16 j + [0, 16)
-      const uint32_t wv[4] = {raw.v[j].x, raw.v[j].y, raw.v[j].z, raw.v[j].w};
-      uint32_t hv[8];
-#pragma unroll
-      for (int k = 0; k < 4; k++) {
-        hv[2 * k] = pa_h2u(__half2(
-            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wv[k] & 0xFFFF), __NV_E4M3)));
-        hv[2 * k + 1] = pa_h2u(
-            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wv[k] >> 16), __NV_E4M3)));
-      }
-      uint8_t* dst = trow + (2 * qq + (j >> 2)) * PA_KB;
-      const int cc = 2 * (j & 3);
-      *reinterpret_cast<uint4*>(dst + ((cc ^ sw) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-      *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ sw) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-    }
-  }
-  return nan;
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// S^T and O^T products; n: query rows of the tile.  P is read MN-major (its
-// rows are keys, the K axis of the second product).
+// S^T (M = 64 keys) and O^T (M = 128 channels) products; n: query rows of the
+// tile.  P is read MN-major (its rows are keys, the K axis of the second
+// product).
 __device__ __forceinline__ uint32_t pa_idesc(int n, bool pv) {
   return (1u << 4) | (pv ? (1u << 15) | (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) |
-         ((128u >> 4) << 24);
+         ((uint32_t)((pv ? 128 : PA_KEYS) >> 4) << 24);
+}
+
+// The run that begins at `tile`: the segment of that tile as far as this CTA's
+// share [.., tile_end) goes.
+__device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan& pl,
+                                             const int* cum, int64_t tile, int64_t tile_end,
+                                             bool stop) {
+  PaRun run;
+  run.valid = tile < tile_end && !stop;
+  if (!run.valid) return run;
+  int64_t seg_end;
+  run.n_win = run.win_lo = 0;
+  if (tile < pl.shared) {
+    const int seg = (int)(tile / pl.prefix_tiles);
+    run.own = false;
+    run.seq = 0;
+    run.row0 = seg * PA_ROWS;
+    run.n_rows = min(PA_ROWS, p.batch * p.nq * CSA2_H - run.row0);
+    run.kt = (int)(tile - (int64_t)seg * pl.prefix_tiles);
+    run.own_tiles = pl.prefix_tiles;
+    run.first_pos = 0;
+    run.slot = pl.shared_slot(seg, blockIdx.x);
+    seg_end = (int64_t)(seg + 1) * pl.prefix_tiles;
+    run.n_keys = p.prefix;
+  } else {
+    const int64_t u = tile - pl.shared;
+    int lo = 0, hi = p.batch;  // the last b with q_blocks * cum[b] <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((int64_t)cum[mid] * pl.q_blocks <= u) lo = mid; else hi = mid;
+    }
+    const int b = lo, kts = cum[b + 1] - cum[b];
+    const int64_t rem = u - (int64_t)cum[b] * pl.q_blocks;
+    const int qb = (int)(rem / kts);
+    run.own = true;
+    run.seq = b;
+    run.row0 = (b * p.nq + qb * PA_QB) * CSA2_H;
+    run.n_rows = min(PA_QB, p.nq - qb * PA_QB) * CSA2_H;
+    run.kt = (int)(rem - (int64_t)qb * kts) - PA_SEG;  // < 0: an empty tile
+    run.own_tiles = kts - PA_SEG - pl.win_tiles;
+    run.first_pos = p.prefix;
+    run.slot = pl.own_slot(b * pl.q_blocks + qb, blockIdx.x);
+    seg_end = tile - run.kt + kts - PA_SEG;
+    const int n = p.n_rows[b];
+    run.n_keys = n < 0 ? 0 : min(n, p.max_rows);
+    if (p.swa) {
+      run.n_win = p.swa_len[b];
+      if (run.n_win < 0 || run.n_win > p.swa_rows) {
+        if ((threadIdx.x & 31) == 0) set_status(p.status, ST_DEVICE_CHECK);
+        run.n_win = run.n_win < 0 ? 0 : p.swa_rows;
+      }
+      run.win_lo = max(0, run.n_win - (p.nq - 1 - qb * PA_QB) - CSA2_W);
+    }
+  }
+  run.kt_end = run.kt + (int)(min(seg_end, tile_end) - tile);
+  run.line = run.kt_end - run.kt;
+  run.kt = max(run.kt, 0);
+  return run;
+}
+
+// The softmax warps bring a run's queries and limits into shared memory.
+__device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& run, PaSmem& s,
+                                           int warp, int lane) {
+      // Q' = Q * 2^e in fp16, max |Q'| of a row in [2^14, 2^15): one warp per row,
+  // 16 channels per lane, four rows' loads in flight
+#pragma unroll 1
+  for (int h0 = warp; h0 < run.n_rows; h0 += 4 * PA_SM_WARPS) {
+    uint4 v[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int h = min(h0 + u * PA_SM_WARPS, run.n_rows - 1);
+      const uint4* src =
+          reinterpret_cast<const uint4*>(p.q + (int64_t)(run.row0 + h) * CSA2_D) + 2 * lane;
+      v[u][0] = __ldg(src);
+      v[u][1] = __ldg(src + 1);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int h = h0 + u * PA_SM_WARPS;
+      if (h >= run.n_rows) break;
+      uint32_t mx = 0u;
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const uint32_t w[4] = {v[u][k].x, v[u][k].y, v[u][k].z, v[u][k].w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) mx = max(mx, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      const int e = q_pow2_exponent(mx);
+      const int e1 = e / 2, e2 = e - e1;
+      const float f = pow2i(e1), f2 = pow2i(e2);
+      // (where 2^-e leaves fp32's range the logits are below 2^-80 anyway)
+      if (lane == 0) s.scl[h] = p.scale_log2 * PA_TILE_SCALE * pow2i(-e1) * pow2i(-e2);
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const uint32_t w[4] = {v[u][k].x, v[u][k].y, v[u][k].z, v[u][k].w};
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          g[2 * j] = __uint_as_float(w[j] << 16) * f * f2;
+          g[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * f * f2;
+        }
+        uint32_t o4[4];  // the tile's order of channels
+#pragma unroll
+        for (int j = 0; j < 4; j++) o4[j] = pa_h2u(__floats2half2_rn(g[j], g[j + 4]));
+        *reinterpret_cast<uint4*>(s.q + (lane >> 2) * PA_QKB + pa_sw(h, 2 * (lane & 3) + k)) =
+            make_uint4(o4[0], o4[1], o4[2], o4[3]);
+      }
+    }
+  }
+  // visible keys of every row: cache positions, and window rows
+  const int t = 32 * warp + lane;
+  if (warp < 2) {
+    int lo[2] = {0, 0}, hi[2] = {0x7FFFFFFF, 0x7FFFFFFF};
+    if (t < run.n_rows) {
+      const int qi = (run.row0 + t) / CSA2_H, b = qi / p.nq, later = p.nq - 1 - (qi - b * p.nq);
+      const int n = p.n_rows[b];
+      hi[0] = min((n < 0 ? 0 : min(n, p.max_rows)) - later, run.n_keys);
+      hi[1] = max(0, run.n_win - later);
+      lo[1] = max(0, run.n_win - later - CSA2_W);
+    }
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+      s.lo[w][t] = lo[w];
+      s.hi[w][t] = hi[w];
+    }
+  }
+  fence_proxy_async_smem();
+  bar_sync<32 * PA_SM_WARPS>(5);
+  if (warp == 0) {  // over all 64 rows
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+      const int a = __reduce_max_sync(0xffffffffu, max(s.lo[w][lane], s.lo[w][lane + 32]));
+      const int z = __reduce_min_sync(0xffffffffu, min(s.hi[w][lane], s.hi[w][lane + 32]));
+      if (lane == 0) {
+        s.lo_max[w] = a;
+        s.hi_min[w] = z;
+      }
+    }
+  }
 }
 
 __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParams p) {
   extern __shared__ uint8_t smem_raw[];
   PaSmem& s = *reinterpret_cast<PaSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
   pdl_launch_dependents();
   if (t == 0) {
-    mbar_init(&s.mbar, 1);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&s.full[i], PA_DQ_WARPS);
+      mbar_init(&s.empty[i], 1);
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], PA_SM_WARPS);
+    }
     fence_mbar_init();
     s.abort = 0;
   }
-  if (warp == 0) {
+  if (warp == PA_MMA_WARP) {
     tmem_alloc(&s.tmem_base, PA_TMEM_COLS);
     tmem_relinquish();
   }
@@ -219,17 +403,20 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   // ---- the plan: prefix sums of the sequences' own key tiles
   PaPlan pl = pa_plan(p);
   {
-    int v[2] = {0, 0};
+    constexpr int PER = (CSA2_PREFIX_MAX_BATCH + PA_NT - 1) / PA_NT;
+    int v[PER], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const int b = 2 * t + k;
+    for (int k = 0; k < PER; k++) {
+      const int b = PER * t + k;
+      v[k] = 0;
       if (b < p.batch) {
         const int n = p.n_rows[b];
         if ((n < 0 || n > p.max_rows) && blockIdx.x == 0) set_status(p.status, ST_DEVICE_CHECK);
-        v[k] = pa_own_tiles(p, n) + pl.win_tiles;
+        v[k] = pa_own_line(p, pl, n);
       }
+      sum += v[k];
     }
-    int incl = v[0] + v[1];
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -239,288 +426,338 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int before = 0;
+    int before = incl - sum;
     for (int w = 0; w < warp; w++) before += s.wsum[w];
-    if (2 * t < p.batch) s.cum[2 * t + 1] = before + incl - v[1];
-    if (2 * t + 1 < p.batch) s.cum[2 * t + 2] = before + incl;
-    if (t == 0) s.cum[0] = 0;
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+      const int b = PER * t + k;
+      if (b < p.batch) s.cum[b] = before;
+      before += v[k];
+      if (b == p.batch - 1) s.cum[p.batch] = before;
+    }
     __syncthreads();
   }
   pl.finish(s.cum[p.batch]);
   const uint32_t tmem = s.tmem_base;
-  const int r = t & (PA_KEYS - 1), qq = t >> 7;  // key row, quarter; also TMEM lane, column group
-  const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
 
-  int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
-  const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
-  bool alive = true;
-  while (tile < tile_end && alive) {
-    // ---- the segment of this tile and the run of it that is ours
-    PaRun run;
-    int n_own, n_win = 0;  // keys of the row map, rows of the window
-    int64_t seg_end;
-    if (tile < pl.shared) {
-      const int seg = (int)(tile / pl.prefix_tiles);
-      run.own = false;
-      run.seq = 0;
-      run.row0 = seg * PA_ROWS;
-      run.n_rows = min(PA_ROWS, p.batch * p.nq * CSA2_H - run.row0);
-      run.kt = (int)(tile - (int64_t)seg * pl.prefix_tiles);
-      run.own_tiles = pl.prefix_tiles;
-      run.first_pos = 0;
-      run.win_lo = 0;
-      run.slot = pl.shared_slot(seg, blockIdx.x);
-      seg_end = (int64_t)(seg + 1) * pl.prefix_tiles;
-      n_own = p.prefix;
-    } else {
-      const int64_t u = tile - pl.shared;
-      int lo = 0, hi = p.batch;  // the last b with q_blocks * cum[b] <= u
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)s.cum[mid] * pl.q_blocks <= u) lo = mid; else hi = mid;
-      }
-      const int b = lo, kts = s.cum[b + 1] - s.cum[b];
-      const int64_t rem = u - (int64_t)s.cum[b] * pl.q_blocks;
-      const int qb = (int)(rem / kts);
-      run.own = true;
-      run.seq = b;
-      run.row0 = (b * p.nq + qb * PA_QB) * CSA2_H;
-      run.n_rows = min(PA_QB, p.nq - qb * PA_QB) * CSA2_H;
-      run.kt = (int)(rem - (int64_t)qb * kts);
-      run.own_tiles = kts - pl.win_tiles;
-      run.first_pos = p.prefix;
-      run.slot = pl.own_slot(b * pl.q_blocks + qb, blockIdx.x);
-      seg_end = tile - run.kt + kts;
-      const int n = p.n_rows[b];
-      n_own = n < 0 ? 0 : min(n, p.max_rows);
-      run.win_lo = 0;
-      if (p.swa) {
-        n_win = p.swa_len[b];
-        if (n_win < 0 || n_win > p.swa_rows) {
-          if (t == 0) set_status(p.status, ST_DEVICE_CHECK);
-          n_win = n_win < 0 ? 0 : p.swa_rows;
-        }
-        run.win_lo = max(0, n_win - (p.nq - 1 - qb * PA_QB) - CSA2_W);
-      }
-    }
-    run.kt_end = run.kt + (int)(min(seg_end, tile_end) - tile);
-    tile += run.kt_end - run.kt;
-
-    PaRaw raw;
-    pa_load(p, run, run.kt, r, qq, n_own, n_win, raw);
-
-    // ---- Q' = Q * 2^e in fp16, max |Q'| of a row in [2^14, 2^15): one warp per
-    // row, 16 channels per lane
-    for (int h = warp; h < run.n_rows; h += PA_NT / 32) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(run.row0 + h) * CSA2_D) +
-                         2 * lane;
-      uint4 v[2];
-      uint32_t mx = 0u;
+  // Per run of tiles: BAR_RUN (the run is known), BAR_Q (its queries are in
+  // shared memory; softmax and MMA warps), the tiles, BAR_RUN (all is done).
+  // Tile i of the CTA uses buffers i & 1; their barriers' phase is (i >> 1) & 1.
+  constexpr int BAR_RUN = 3, BAR_Q = 4;
+  constexpr int Q_THREADS = 32 * (PA_SM_WARPS + 1);
+  uint32_t i = 0;
+  if (warp < PA_DQ_WARPS) {
+    // ------------------------------------------------ key tiles to fp16
+    // Lane (seg, r8) of a warp has key r8 of the warp's eight and 32 channels (16
+    // code bytes) of each 128-channel block: a load of the warp touches 8 rows by
+    // 64 consecutive bytes, and a quarter-warp's 16-byte stores go to 8 rows,
+    // whose swizzle gives them different banks.  The next tile's codes are loaded
+    // as each block is done with.
+    const int seg = lane >> 3, r = 8 * warp + (lane & 7), sw = lane & 7, cc = 4 * (seg & 1);
+    for (;;) {
+      bar_sync<PA_NT>(BAR_RUN);
+      const PaRun run = s.run;
+      if (!run.valid) break;
+      uint4 v[4];      // by block
+      uint32_t sc[4];  // the two scales of the same 32 channels
+      auto load = [&](int64_t row, int b) {
+        v[b] = ld_now_v4(p.codes + row * (CSA2_D / 2) + 64 * b + 16 * seg);
+        sc[b] = ld_now_u16(p.scales + row * (CSA2_D / 16) + 8 * b + 2 * seg);
+      };
+      int64_t row = pa_row(p, run, run.kt, r);
 #pragma unroll
-      for (int k = 0; k < 2; k++) {
-        v[k] = __ldg(src + k);
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) mx = max(mx, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+      for (int b = 0; b < 4; b++) {
+        v[b] = make_uint4(0u, 0u, 0u, 0u);
+        sc[b] = 0u;
+        if (row >= 0) load(row, b);
       }
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      const int e = q_pow2_exponent(mx);
-      const int e1 = e / 2, e2 = e - e1;
-      const float f = pow2i(e1), f2 = pow2i(e2);
-      if (lane == 0) {
-        s.scl1[h] = pow2i(-e1);
-        s.scl2[h] = p.scale_log2 * pow2i(-e2);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; k++) {
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t o4[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          o4[j] = pa_h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * f * f2,
-                                           __uint_as_float(w[j] & 0xFFFF0000u) * f * f2));
-        *reinterpret_cast<uint4*>(s.q + (lane >> 2) * PA_QKB + pa_sw(h, 2 * (lane & 3) + k)) =
-            make_uint4(o4[0], o4[1], o4[2], o4[3]);
-      }
-    }
-    float l[16];
-#pragma unroll
-    for (int j = 0; j < 16; j++) l[j] = 0.0f;
-    if (t < PA_ROWS) s.m[t] = PA_NONE;
-    bool window_limits = false;
-    const int kt0 = run.kt;
+      int64_t next = pa_row(p, run, run.kt + 1, r);
+      const int kt_cache = run.own ? min(run.own_tiles, run.kt_end) : run.kt_end;
+      int kt = run.kt;
 #pragma unroll 1
-    for (int kt = kt0; kt < run.kt_end && alive; kt++) {
-      // ---- visible keys of every row: positions, or window rows
-      const bool win = run.own && kt >= run.own_tiles;
-      if ((kt == kt0 || win != window_limits) && t < run.n_rows) {
-        const int qi = (run.row0 + t) / CSA2_H, b = qi / p.nq, later = p.nq - 1 - (qi - b * p.nq);
-        if (win) {
-          s.hi[t] = max(0, n_win - later);
-          s.lo[t] = max(0, n_win - later - CSA2_W);
-        } else {
-          const int n = p.n_rows[b];
-          s.hi[t] = min((n < 0 ? 0 : min(n, p.max_rows)) - later, n_own);
-          s.lo[t] = 0;
+      for (; kt < kt_cache; kt++, i++) {
+        const int64_t after = pa_row(p, run, kt + 2, r);
+        // A key that is not there, or whose values hold a NaN, becomes zeros: the
+        // P = 0 of a row that must not see it would turn NaN in the product
+        const bool nan = has_nan(sc[0] | (sc[1] << 16)) || has_nan(sc[2] | (sc[3] << 16));
+        const bool zero = row < 0 || nan;
+        uint8_t* dst = s.tile[i & 1] + (seg >> 1) * PA_KB + r * 128;
+        if (i >= 2) mbar_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
+        s.key[i & 1][r][seg] = (uint8_t)(row < 0 ? 1 : (nan ? 2 : 0));
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          if (!zero) {
+            pa_put_fp4(dst + 2 * b * PA_KB, sw, cc, v[b], sc[b]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+              *reinterpret_cast<uint4*>(dst + 2 * b * PA_KB + (((cc + c) ^ sw) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          if (next >= 0) load(next, b);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[i & 1]);
+        row = next;
+        next = after;
       }
-      window_limits = win;
-      // ---- the fp16 tile
-      reinterpret_cast<uint8_t*>(&s.bad[r])[qq] = pa_dequant(raw, s.tile, r, qq);
-      const bool key_ok = raw.ok;
-      const int key = win ? run.win_lo + (kt - run.own_tiles) * PA_KEYS + r
-                          : run.first_pos + kt * PA_KEYS + r;
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      // ---- S^T = K Q'^T: K = 512 in 32 steps
-      if (t == 0) {
+#pragma unroll 1
+      for (; kt < run.kt_end; kt++, i++) {  // window tiles
+        const int w = run.win_lo + (kt - run.own_tiles) * PA_KEYS + r;
+        uint4 a[8];
+        bool nan = false;
+#pragma unroll
+        for (int b = 0; b < 8; b++) a[b] = make_uint4(0u, 0u, 0u, 0u);
+        if (w < run.n_win) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.swa + ((int64_t)run.seq * p.swa_rows + w) * CSA2_D + 32 * seg);
+#pragma unroll
+          for (int b = 0; b < 8; b++) a[b] = __ldg(src + 8 * (b >> 1) + (b & 1));
+#pragma unroll
+          for (int b = 0; b < 8; b++)
+            nan |= has_nan(a[b].x) || has_nan(a[b].y) || has_nan(a[b].z) || has_nan(a[b].w);
+        }
+        uint8_t* dst = s.tile[i & 1] + (seg >> 1) * PA_KB + r * 128;
+        if (i >= 2) mbar_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
+        s.key[i & 1][r][seg] = (uint8_t)(w >= run.n_win ? 1 : (nan ? 2 : 0));
+#pragma unroll
+        for (int b = 0; b < 8; b++) {
+          if (nan) a[b] = make_uint4(0u, 0u, 0u, 0u);
+          uint8_t* d = dst + 2 * (b >> 1) * PA_KB;
+          const int c = cc + 2 * (b & 1);
+          *reinterpret_cast<uint4*>(d + ((c ^ sw) << 4)) = pa_e4m3x8(a[b].x, a[b].y);
+          *reinterpret_cast<uint4*>(d + (((c + 1) ^ sw) << 4)) = pa_e4m3x8(a[b].z, a[b].w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[i & 1]);
+      }
+      bar_sync<PA_NT>(BAR_RUN);
+    }
+  } else if (warp < PA_MMA_WARP) {
+    // --------------------------------------------------------- softmax
+    // Warp (quad, half): keys 16 quad + [0, 16), query rows 32 half + [0, 32).  An
+    // M = 64 accumulator has its rows in lanes 0..15 of each TMEM quarter; read as
+    // 16 x 256 bits, a thread holds keys lane / 4 and lane / 4 + 8 by columns
+    // 8 n + 2 (lane % 4) + {0, 1}.
+    const int w = warp - PA_DQ_WARPS, quad = w & 3, half = w >> 2;
+    const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
+    const int c0 = 32 * half + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
+    int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
+    const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
+    for (;;) {
+      if (w == 0) {
+        PaRun r;
+        do {  // skips what holds empty tiles only
+          r = pa_next_run(p, pl, s.cum, tile, tile_end, s.abort != 0);
+          if (r.valid) tile += r.line;
+        } while (r.valid && r.kt_end <= r.kt);
+        if (lane == 0) s.run = r;
+      }
+      bar_sync<PA_NT>(BAR_RUN);
+      const PaRun run = s.run;
+      if (!run.valid) break;
+      pa_queries(p, run, s, w, lane);
+      bar_sync<Q_THREADS>(BAR_Q);
+      const bool active = 32 * half < run.n_rows;  // per warp
+      float scl[8], m[8], l[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int c = c0 + 8 * (j >> 1) + (j & 1);
+        scl[j] = c < run.n_rows ? s.scl[c] : 0.0f;
+        m[j] = PA_NONE;
+        l[j] = 0.0f;
+      }
+#pragma unroll 1
+      for (int kt = run.kt; kt < run.kt_end; kt++, i++) {
+        const bool win = run.own && kt >= run.own_tiles;
+        const int first = win ? run.win_lo + (kt - run.own_tiles) * PA_KEYS
+                              : run.first_pos + kt * PA_KEYS;
+        if (!mbar_wait(&s.s_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
+        mbar_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort);  // (complete) the keys' flags
+        __syncwarp();
         tc_fence_after();
-        const uint64_t da = sdesc_k128(smem_u32(s.tile)), db = sdesc_k128(smem_u32(s.q));
-        const uint32_t id = pa_idesc(run.n_rows, false);
+        if (active) {
+          uint32_t acc[16];
+          tmem_ld_16x256b_x4(tmem + lane_base + PA_S_COL + PA_ROWS * (i & 1) + 32 * half, acc);
+          const uint32_t f0 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0]);
+          const uint32_t f1 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0 + 8]);
+          const bool plain = first >= s.lo_max[win] && first + PA_KEYS <= s.hi_min[win] &&
+                             __all_sync(0xffffffffu, (f0 | f1) == 0);
+          tmem_ld_wait();
+          // x[4 n + 2 k + e]: key k0 + 8 k, row c0 + 8 n + e
+          float x[16];
+#pragma unroll
+          for (int j = 0; j < 16; j++)
+            x[j] = __uint_as_float(acc[j]) * scl[2 * (j >> 2) + (j & 1)];
+          if (!plain) {
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+              const int c = c0 + 8 * (j >> 2) + (j & 1), key = first + k0 + 8 * ((j >> 1) & 1);
+              const uint32_t f = (j >> 1) & 1 ? f1 : f0;
+              const bool see = !(f & 1u) && key >= s.lo[win][c] && key < s.hi[win][c];
+              x[j] = see ? (f ? __int_as_float(0x7FC00000) : x[j]) : -INFINITY;
+            }
+          }
+          float over = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; j++) over = fmaxf(over, x[j] - m[2 * (j >> 2) + (j & 1)]);
+          if (bar_or_128(1 + half, over > PA_SHIFT + PA_SLACK)) {
+            // some logit is far above its reference: raise the references to the
+            // rows' maxima and scale what was summed
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              float mx = fmaxf(x[4 * (j >> 1) + (j & 1)], x[4 * (j >> 1) + 2 + (j & 1)]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              if (lane < 4) s.red[quad][c0 + 8 * (j >> 1) + (j & 1)] = mx;
+            }
+            bar_or_128(1 + half, false);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              const int c = c0 + 8 * (j >> 1) + (j & 1);
+              const float mx = fmaxf(fmaxf(s.red[0][c], s.red[1][c]), fmaxf(s.red[2][c], s.red[3][c]));
+              const float top = fmaxf(m[j], mx - PA_SHIFT), f = ex2(m[j] - top);
+              m[j] = top;
+              l[j] *= f;
+              if (quad == 0 && lane < 4) s.fac[c] = f;
+            }
+            bar_or_128(1 + half, false);
+            if (kt != run.kt) {
+              // the products up to the last tile's are in O
+              if (!mbar_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
+              __syncwarp();
+              tc_fence_after();
 #pragma unroll 1
-        for (uint32_t i = 0; i < 32; i++)
-          umma_bf16(tmem + PA_S_COL, da + (((i >> 2) * PA_KB + 32 * (i & 3)) >> 4),
-                    db + (((i >> 2) * PA_QKB + 32 * (i & 3)) >> 4), id, i != 0);
-        umma_commit(&s.mbar);
+              for (int g = 0; g < 8; g++) {  // channel block g / 2, 16 of the 32 rows
+                const int c = 32 * half + 16 * (g & 1);
+                const uint32_t at = tmem + lane_base + 64 * (g >> 1) + c;
+                uint32_t o[16];
+                tmem_ld_x16(at, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * s.fac[c + j]);
+                tmem_st_x16(at, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          uint8_t* dst = s.p[i & 1] + k0 * 128 + 4 * (lane & 3);
+#pragma unroll
+          for (int n = 0; n < 4; n++) {
+            const float p0 = ex2(x[4 * n] - m[2 * n]), p1 = ex2(x[4 * n + 1] - m[2 * n + 1]);
+            const float p2 = ex2(x[4 * n + 2] - m[2 * n]), p3 = ex2(x[4 * n + 3] - m[2 * n + 1]);
+            l[2 * n] += p0 + p2;
+            l[2 * n + 1] += p1 + p3;
+            const uint32_t at = (uint32_t)((4 * half + n) ^ (k0 & 7)) << 4;  // (k0 + 8 alike)
+            *reinterpret_cast<uint32_t*>(dst + at) = pa_h2u(__floats2half2_rn(p0, p1));
+            *reinterpret_cast<uint32_t*>(dst + 1024 + at) = pa_h2u(__floats2half2_rn(p2, p3));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[i & 1]);
       }
-      if (kt + 1 < run.kt_end) pa_load(p, run, kt + 1, r, qq, n_own, n_win, raw);
-      if (!mbar_wait(&s.mbar, 0, nullptr)) s.abort = 1;
+      // ---- the run's partial: O [row][channel], (max, sum) per row.  The last
+      // tile's commit covers every product.
+      if (!mbar_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
       __syncwarp();
       tc_fence_after();
-      // ---- softmax: one key and 16 query rows per thread
-      const bool active = 16 * qq < run.n_rows;  // per warp
-      float x[16];
-      float over = -INFINITY;
       if (active) {
-        uint32_t acc[16];
-        tmem_ld_x16(tmem + lane_base + PA_S_COL + 16 * qq, acc);
-        tmem_ld_wait();
-        const bool bad = s.bad[r] != 0;
-#pragma unroll
-        for (int j = 0; j < 16; j++) {
-          const int c = 16 * qq + j;
-          const bool see = key_ok && key >= s.lo[c] && key < s.hi[c];
-          const float v = __uint_as_float(acc[j]) * s.scl1[c] * s.scl2[c];
-          x[j] = see ? (bad ? __int_as_float(0x7FC00000) : v) : -INFINITY;
-          over = fmaxf(over, x[j] - s.m[c]);
-        }
-      }
-      if (__syncthreads_or(over > PA_SLACK)) {
-        // some logit is far above its reference: raise the references to the
-        // rows' maxima and scale what was summed
-        if (active) {
-#pragma unroll
-          for (int j = 0; j < 16; j++) {
-            const float mx = warp_max_f32(x[j]);
-            if (lane == 0) s.red[warp & 3][16 * qq + j] = mx;
-          }
-        }
-        __syncthreads();
-        if (active) {
-          float f[16];
-#pragma unroll
-          for (int j = 0; j < 16; j++) {
-            const int c = 16 * qq + j;
-            const float old = s.m[c];
-            const float mx = fmaxf(fmaxf(s.red[0][c], s.red[1][c]), fmaxf(s.red[2][c], s.red[3][c]));
-            f[j] = exp2f(old - fmaxf(old, mx));
-            l[j] *= f[j];
-          }
-          if (kt != kt0) {
-#pragma unroll 1
-            for (int cb = 0; cb < 4; cb++) {
-              uint32_t o[16];
-              tmem_ld_x16(tmem + lane_base + 64 * cb + 16 * qq, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j]);
-              tmem_st_x16(tmem + lane_base + 64 * cb + 16 * qq, o);
-            }
-            tmem_st_wait();
-          }
-        }
-        __syncthreads();
-        if (t < run.n_rows)
-          s.m[t] = fmaxf(s.m[t], fmaxf(fmaxf(s.red[0][t], s.red[1][t]),
-                                       fmaxf(s.red[2][t], s.red[3][t])));
-        __syncthreads();
-      }
-      if (active) {
-        uint32_t hv[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const int c = 16 * qq + 2 * j;
-          const __half2 h = __floats2half2_rn(exp2f(x[2 * j] - s.m[c] + PA_SHIFT),
-                                              exp2f(x[2 * j + 1] - s.m[c + 1] + PA_SHIFT));
-          const float2 g = __half22float2(h);
-          l[2 * j] += g.x;
-          l[2 * j + 1] += g.y;
-          hv[j] = pa_h2u(h);
+          float v = l[j];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane < 4) {
+            const int c = c0 + 8 * (j >> 1) + (j & 1);
+            s.red[quad][c] = v;
+            if (quad == 0) s.fac[c] = m[j];
+          }
         }
-        *reinterpret_cast<uint4*>(s.p + pa_sw(r, 2 * qq)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *reinterpret_cast<uint4*>(s.p + pa_sw(r, 2 * qq + 1)) =
-            make_uint4(hv[4], hv[5], hv[6], hv[7]);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      // ---- O^T += V^T P^T: four channel blocks of 128, K = 128 keys in 8 steps
-      if (t == 0) {
-        tc_fence_after();
-        const uint64_t da = sdesc_mn128(smem_u32(s.tile), PA_KB, 1024),
-                       db = sdesc_mn128(smem_u32(s.p), PA_KEYS * 128, 1024);
-        const uint32_t id = pa_idesc(run.n_rows, true);
-#pragma unroll 1
-        for (uint32_t i = 0; i < 32; i++) {
-          const uint32_t cb = i & 3, ks = i >> 2;
-          umma_bf16(tmem + 64 * cb, da + ((cb * 2 * PA_KB + ks * 2048) >> 4),
-                    db + ((ks * 2048) >> 4), id, kt != kt0 || ks != 0);
+        bar_or_128(1 + half, false);
+        const int c = 32 * half + lane;
+        if (quad == 0 && c < run.n_rows) {
+          p.part_ml[2 * (run.slot + c)] = s.fac[c];
+          p.part_ml[2 * (run.slot + c) + 1] =
+              (s.red[0][c] + s.red[1][c]) + (s.red[2][c] + s.red[3][c]);
         }
-        umma_commit(&s.mbar);
+#pragma unroll 2
+        for (int g = 0; g < 8; g++) {  // channel block g / 2, 16 of the 32 rows
+          const int r0 = 32 * half + 16 * (g & 1);
+          if (r0 >= run.n_rows) continue;
+          uint32_t o[16];
+          tmem_ld_x16(tmem + lane_base + 64 * (g >> 1) + r0, o);
+          tmem_ld_wait();
+          float* dst = p.part_o + (run.slot + r0) * CSA2_D + 128 * (g >> 1) +
+                       pa_channel(32 * quad + lane);
+#pragma unroll
+          for (int j = 0; j < 16; j++) dst[j * CSA2_D] = __uint_as_float(o[j]) * PA_TILE_SCALE;
+        }
+        tc_fence_before();
       }
-      if (!mbar_wait(&s.mbar, 1, nullptr)) s.abort = 1;
-      __syncwarp();
+      bar_sync<PA_NT>(BAR_RUN);
+    }
+  } else {
+    // ------------------------------------------------------ the products
+    const uint64_t qd = sdesc_k128(smem_u32(s.q));
+    const uint64_t pd = sdesc_mn128(smem_u32(s.p[0]), PA_KEYS * 128, 1024);
+    const uint64_t kd = sdesc_k128(smem_u32(s.tile[0]));
+    const uint64_t vd = sdesc_mn128(smem_u32(s.tile[0]), PA_KB, 1024);
+    for (;;) {
+      bar_sync<PA_NT>(BAR_RUN);
+      const int n_tiles = s.run.kt_end - s.run.kt, n_rows = s.run.n_rows;
+      if (!s.run.valid) break;
+      bar_sync<Q_THREADS>(BAR_Q);
       tc_fence_after();
-      __syncthreads();
-      alive = s.abort == 0;
-    }
-    if (!alive) {
-      if (t == 0) set_status(p.status, ST_TIMEOUT);
-      break;
-    }
-
-    // ---- the run's partial: O [row][channel], (max, sum) per row
-    if (16 * qq < run.n_rows) {
+      const uint32_t id_s = pa_idesc(n_rows, false), id_o = pa_idesc(n_rows, true);
+      const bool leader = elect_one();
+      // S^T = K Q'^T of tile j: K = 512 in 32 steps
+      auto logits = [&](uint32_t j) {
+        if (!mbar_wait(&s.full[j & 1], (j >> 1) & 1, &s.abort)) s.abort = 1;
+        __syncwarp();
+        tc_fence_after();
+        if (leader) {
+          const uint64_t a = kd + ((j & 1) * ((8 * PA_KB) >> 4));
+          const uint32_t d = tmem + PA_S_COL + PA_ROWS * (j & 1);
 #pragma unroll
-      for (int j = 0; j < 16; j++) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], o);
-        if (lane == 0) s.red[warp & 3][16 * qq + j] = l[j];
-      }
+          for (uint32_t k = 0; k < 32; k++)
+            umma_bf16(d, a + (((k >> 2) * PA_KB + 32 * (k & 3)) >> 4),
+                      qd + (((k >> 2) * PA_QKB + 32 * (k & 3)) >> 4), id_s, k != 0);
+          umma_commit(&s.s_full[j & 1]);
+        }
+        __syncwarp();
+      };
+      logits(i);
 #pragma unroll 1
-      for (int cb = 0; cb < 4; cb++) {
-        uint32_t o[16];
-        tmem_ld_x16(tmem + lane_base + 64 * cb + 16 * qq, o);
-        tmem_ld_wait();
-        float* dst = p.part_o + (run.slot + 16 * qq) * CSA2_D + 128 * cb + r;
+      for (int k = 0; k < n_tiles; k++, i++) {
+        if (k + 1 < n_tiles) logits(i + 1);  // while the softmax of tile i runs
+        if (!mbar_wait(&s.p_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
+        __syncwarp();
+        tc_fence_after();
+        // O^T += V^T P^T: four channel blocks, K = 64 keys in four steps
+        if (leader) {
+          const uint64_t a = vd + ((i & 1) * ((8 * PA_KB) >> 4));
+          const uint64_t b = pd + ((i & 1) * ((PA_KEYS * 128) >> 4));
 #pragma unroll
-        for (int j = 0; j < 16; j++) dst[j * CSA2_D] = __uint_as_float(o[j]);
+          for (uint32_t j = 0; j < 16; j++)
+            umma_bf16(tmem + 64 * (j & 3), a + (((j & 3) * 2 * PA_KB + (j >> 2) * 2048) >> 4),
+                      b + (((j >> 2) * 2048) >> 4), id_o, k != 0 || j >= 4);
+          umma_commit(&s.empty[i & 1]);
+        }
+        __syncwarp();
       }
+      bar_sync<PA_NT>(BAR_RUN);
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (t < run.n_rows) {
-      p.part_ml[2 * (run.slot + t)] = s.m[t];
-      p.part_ml[2 * (run.slot + t) + 1] =
-          (s.red[0][t] + s.red[1][t]) + (s.red[2][t] + s.red[3][t]);
-    }
-    __syncthreads();
   }
+  if (s.abort && t == 0) set_status(p.status, ST_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == PA_MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, PA_TMEM_COLS);
   }
@@ -546,7 +783,7 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   PaPlan pl = pa_plan(p);
   int before = 0, all = 0;
   for (int i = t; i < p.batch; i += PM_NT) {
-    const int k = pa_own_tiles(p, p.n_rows[i]) + pl.win_tiles;
+    const int k = pa_own_line(p, pl, p.n_rows[i]);
     all += k;
     if (i < b) before += k;
   }
@@ -558,7 +795,7 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   }
   __syncthreads();
   pl.finish(sums[0]);
-  const int kts = pa_own_tiles(p, p.n_rows[b]) + pl.win_tiles;
+  const int kts = pa_own_line(p, pl, p.n_rows[b]);
 
   // ---- the row's partials: shared segment, then own segment
   const int qb = tq / PA_QB, seg = row / PA_ROWS, oseg = b * pl.q_blocks + qb;
@@ -578,7 +815,7 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   int64_t at = 0;
   if (t < n) {  // n <= 2 * PA_MAX_GRID <= PM_NT
     const int k = t < count[0] ? 0 : 1, c = first[k] + (k ? t - count[0] : t);
-    const int64_t a = max(pl.tile_at(c), ts[k]), z = min(pl.tile_at(c + 1), te[k]);
+    const int64_t a = max(pl.tile_at(c), ts[k] + (k ? PA_SEG : 0)), z = min(pl.tile_at(c + 1), te[k]);
     if (a < z) {
       at = k ? pl.own_slot(oseg, c) + (tq - qb * PA_QB) * CSA2_H + row % CSA2_H
              : pl.shared_slot(seg, c) + row % PA_ROWS;
@@ -648,7 +885,7 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
 int prefix_grid(const PrefixParams& p, int num_sms) {
   const PaPlan pl = pa_plan(p);
   const int64_t own = (int64_t)p.batch * pl.q_blocks *
-                      ((p.max_rows - p.prefix + PA_KEYS - 1) / PA_KEYS + pl.win_tiles);
+                      ((p.max_rows - p.prefix + PA_KEYS - 1) / PA_KEYS + pl.win_tiles + PA_SEG);
   const int64_t most = num_sms < PA_MAX_GRID ? num_sms : PA_MAX_GRID;
   const int64_t tiles = pl.shared + own;
   return (int)(tiles < 1 ? 1 : (tiles < most ? tiles : most));

@@ -1,14 +1,15 @@
 // prefix_plan.cuh -- how csa2_prefix_attn cuts its work, the same arithmetic
 // for the kernel that computes the partials and the one that merges them.
 //
-// A tile is 128 keys against up to 64 query rows (a row is one head of one
+// A tile is 64 keys against up to 64 query rows (a row is one head of one
 // query).  A segment is every key tile of one row block: first the blocks of 64
 // rows of the whole batch against the shared prefix, then, per sequence, its
 // blocks of up to four queries against its own rows and its window.  The tiles
 // lie on one line in segment order, each as long as it costs, and CTA i of G
 // takes the tiles that start in [i C / G, (i + 1) C / G): every CTA gets an
 // equal share whatever the lengths, and one partial per segment that it touches.
-// (segment + CTA) rises along the line, so it numbers the partials.
+// (segment + CTA) rises along the line, so it numbers the partials.  An own
+// segment begins with PA_SEG empty tiles: what starting and ending it costs.
 #pragma once
 
 #include <stdint.h>
@@ -17,10 +18,11 @@
 
 namespace csa2 {
 
-constexpr int PA_KEYS = 128;     // keys per tile: the MMA's M
+constexpr int PA_KEYS = 64;      // keys per tile: the MMA's M
 constexpr int PA_ROWS = 64;      // query rows per tile: the MMA's N
 constexpr int PA_QB = PA_ROWS / CSA2_H;  // queries per row block
 constexpr int PA_MAX_GRID = 192;
+constexpr int PA_SEG = 3;
 
 // What a tile of n rows costs, relative to others.
 __host__ __device__ inline int pa_cost(int n_rows) { return 12 + n_rows / 16; }
@@ -69,7 +71,8 @@ __host__ __device__ inline PaPlan pa_plan(const PrefixParams& p) {
   pl.q_blocks = (p.nq + PA_QB - 1) / PA_QB;
   pl.own_rows = CSA2_H * (p.nq < PA_QB ? p.nq : PA_QB);
   // the windows of a block of k queries span 128 + k - 1 rows
-  pl.win_tiles = p.swa == nullptr ? 0 : (p.nq == 1 ? 1 : 2);
+  pl.win_tiles =
+      p.swa == nullptr ? 0 : (CSA2_W + (p.nq < PA_QB ? p.nq : PA_QB) - 1 + PA_KEYS - 1) / PA_KEYS;
   pl.shared = pl.row_blocks * pl.prefix_tiles;
   pl.cost_p = pa_cost(rows < PA_ROWS ? rows : PA_ROWS);
   pl.cost_o = pa_cost(pl.own_rows);
@@ -82,6 +85,12 @@ __host__ __device__ inline PaPlan pa_plan(const PrefixParams& p) {
 __host__ __device__ inline int pa_own_tiles(const PrefixParams& p, int n_rows) {
   const int n = n_rows < 0 ? 0 : (n_rows > p.max_rows ? p.max_rows : n_rows);
   return n > p.prefix ? (n - p.prefix + PA_KEYS - 1) / PA_KEYS : 0;
+}
+
+// Tiles of an own segment of sequence b on the line, the empty ones included.
+__host__ __device__ inline int pa_own_line(const PrefixParams& p, const PaPlan& pl, int n_rows) {
+  const int n = pa_own_tiles(p, n_rows) + pl.win_tiles;
+  return n > 0 ? n + PA_SEG : 0;
 }
 
 }  // namespace csa2

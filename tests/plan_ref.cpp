@@ -24,7 +24,7 @@ extern "C" int plan_check(int batch, int nq, int prefix, int max_rows, const int
   p.grid = grid;
   PaPlan pl = pa_plan(p);
   std::vector<int> cum(batch + 1, 0);
-  for (int b = 0; b < batch; b++) cum[b + 1] = cum[b] + pa_own_tiles(p, n_rows[b]) + pl.win_tiles;
+  for (int b = 0; b < batch; b++) cum[b + 1] = cum[b] + pa_own_line(p, pl, n_rows[b]);
   pl.finish(cum[batch]);
   const int64_t tiles = pl.shared + (int64_t)cum[batch] * pl.q_blocks;
   if (tiles == 0) return pl.total == 0 ? 0 : 1;
@@ -46,8 +46,10 @@ extern "C" int plan_check(int batch, int nq, int prefix, int max_rows, const int
   std::set<std::pair<int64_t, int64_t>> taken;
   auto segment = [&](int64_t ts, int64_t te, int seg, bool own) {
     if (te <= ts) return 0;
+    const int64_t real = own ? ts + PA_SEG : ts;
+    if (real >= te) return 8;
     for (int c = pl.cta_of(ts); c <= pl.cta_of(te - 1); c++) {
-      if (!(std::max(at[c], ts) < std::min(at[c + 1], te))) continue;
+      if (!(std::max(at[c], real) < std::min(at[c + 1], te))) continue;
       const int64_t s = own ? pl.own_slot(seg, c) : pl.shared_slot(seg, c);
       const int64_t n = own ? pl.own_rows : PA_ROWS;
       if (s < 0 || s + n > rows) return 5;
