@@ -30,7 +30,12 @@ namespace csa2 {
 // filled, multiplied and filled again, took twice as long.
 constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 8;
 constexpr int PA_MMA_WARP = PA_DQ_WARPS + PA_SM_WARPS;
-constexpr int PA_NT = 32 * (PA_MMA_WARP + 1);
+constexpr int PA_RUN_NT = 32 * (PA_MMA_WARP + 1);  // threads with a role
+constexpr int PA_NT = 32 * (PA_MMA_WARP + 4);      // whole warpgroups: registers move between them
+// Registers per thread: launched with 96 (640 threads), then 256 x 88 + 256 x 112
+// + 128 x 80 = 61,440, the launch's.  With 96 for all, the loops' spills missed
+// the little L1 that the shared memory leaves and cost most of their time.
+constexpr int PA_DQ_REGS = 88, PA_SM_REGS = 112, PA_MMA_REGS = 80;
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
 constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
 constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
@@ -111,6 +116,18 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+// Whether a phase is complete, without waiting, the same for the whole warp.
+__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -451,32 +468,45 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     // Lane (seg, r8) of a warp has key r8 of the warp's eight and 32 channels (16
     // code bytes) of each 128-channel block: a load of the warp touches 8 rows by
     // 64 consecutive bytes, and a quarter-warp's 16-byte stores go to 8 rows,
-    // whose swizzle gives them different banks.  The next tile's codes are loaded
-    // as each block is done with.
+    // whose swizzle gives them different banks.  The next tile's codes are on
+    // their way while this one's wait for a free buffer and are turned.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_DQ_REGS));
     const int seg = lane >> 3, r = 8 * warp + (lane & 7), sw = lane & 7, cc = 4 * (seg & 1);
     for (;;) {
-      bar_sync<PA_NT>(BAR_RUN);
+      bar_sync<PA_RUN_NT>(BAR_RUN);
       const PaRun run = s.run;
       if (!run.valid) break;
-      uint4 v[4];      // by block
-      uint32_t sc[4];  // the two scales of the same 32 channels
-      auto load = [&](int64_t row, int b) {
-        v[b] = ld_now_v4(p.codes + row * (CSA2_D / 2) + 64 * b + 16 * seg);
-        sc[b] = ld_now_u16(p.scales + row * (CSA2_D / 16) + 8 * b + 2 * seg);
+      uint4 v[4], nv[4];       // by block: this tile's codes, the next one's
+      uint32_t sc[4], nsc[4];  // the two scales of the same 32 channels
+      auto load = [&](int64_t row) {
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          if (row >= 0) {
+            nv[b] = ld_now_v4(p.codes + row * (CSA2_D / 2) + 64 * b + 16 * seg);
+            nsc[b] = ld_now_u16(p.scales + row * (CSA2_D / 16) + 8 * b + 2 * seg);
+          }
+        }
       };
-      int64_t row = pa_row(p, run, run.kt, r);
 #pragma unroll
       for (int b = 0; b < 4; b++) {
-        v[b] = make_uint4(0u, 0u, 0u, 0u);
-        sc[b] = 0u;
-        if (row >= 0) load(row, b);
+        nv[b] = make_uint4(0u, 0u, 0u, 0u);
+        nsc[b] = 0u;
       }
-      int64_t next = pa_row(p, run, run.kt + 1, r);
+      int64_t row, next = pa_row(p, run, run.kt, r), after = pa_row(p, run, run.kt + 1, r);
+      load(next);
       const int kt_cache = run.own ? min(run.own_tiles, run.kt_end) : run.kt_end;
       int kt = run.kt;
 #pragma unroll 1
       for (; kt < kt_cache; kt++, i++) {
-        const int64_t after = pa_row(p, run, kt + 2, r);
+        row = next;
+        next = after;
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          v[b] = nv[b];
+          sc[b] = nsc[b];
+        }
+        load(next);
+        after = pa_row(p, run, kt + 2, r);
         // A key that is not there, or whose values hold a NaN, becomes zeros: the
         // P = 0 of a row that must not see it would turn NaN in the product
         const bool nan = has_nan(sc[0] | (sc[1] << 16)) || has_nan(sc[2] | (sc[3] << 16));
@@ -494,13 +524,10 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
               *reinterpret_cast<uint4*>(dst + 2 * b * PA_KB + (((cc + c) ^ sw) << 4)) =
                   make_uint4(0, 0, 0, 0);
           }
-          if (next >= 0) load(next, b);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[i & 1]);
-        row = next;
-        next = after;
       }
 #pragma unroll 1
       for (; kt < run.kt_end; kt++, i++) {  // window tiles
@@ -533,7 +560,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[i & 1]);
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      bar_sync<PA_RUN_NT>(BAR_RUN);
     }
   } else if (warp < PA_MMA_WARP) {
     // --------------------------------------------------------- softmax
@@ -541,6 +568,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     // M = 64 accumulator has its rows in lanes 0..15 of each TMEM quarter; read as
     // 16 x 256 bits, a thread holds keys lane / 4 and lane / 4 + 8 by columns
     // 8 n + 2 (lane % 4) + {0, 1}.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_SM_REGS));
     const int w = warp - PA_DQ_WARPS, quad = w & 3, half = w >> 2;
     const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
     const int c0 = 32 * half + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
@@ -555,7 +583,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         } while (r.valid && r.kt_end <= r.kt);
         if (lane == 0) s.run = r;
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      bar_sync<PA_RUN_NT>(BAR_RUN);
       const PaRun run = s.run;
       if (!run.valid) break;
       pa_queries(p, run, s, w, lane);
@@ -700,58 +728,71 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         }
         tc_fence_before();
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      bar_sync<PA_RUN_NT>(BAR_RUN);
     }
   } else {
     // ------------------------------------------------------ the products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_MMA_REGS));
     const uint64_t qd = sdesc_k128(smem_u32(s.q));
     const uint64_t pd = sdesc_mn128(smem_u32(s.p[0]), PA_KEYS * 128, 1024);
     const uint64_t kd = sdesc_k128(smem_u32(s.tile[0]));
     const uint64_t vd = sdesc_mn128(smem_u32(s.tile[0]), PA_KB, 1024);
-    for (;;) {
-      bar_sync<PA_NT>(BAR_RUN);
+    while (warp == PA_MMA_WARP) {  // (the warpgroup's other warps have no work)
+      bar_sync<PA_RUN_NT>(BAR_RUN);
       const int n_tiles = s.run.kt_end - s.run.kt, n_rows = s.run.n_rows;
       if (!s.run.valid) break;
       bar_sync<Q_THREADS>(BAR_Q);
       tc_fence_after();
       const uint32_t id_s = pa_idesc(n_rows, false), id_o = pa_idesc(n_rows, true);
       const bool leader = elect_one();
-      // S^T = K Q'^T of tile j: K = 512 in 32 steps
-      auto logits = [&](uint32_t j) {
-        if (!mbar_wait(&s.full[j & 1], (j >> 1) & 1, &s.abort)) s.abort = 1;
-        __syncwarp();
-        tc_fence_after();
-        if (leader) {
-          const uint64_t a = kd + ((j & 1) * ((8 * PA_KB) >> 4));
-          const uint32_t d = tmem + PA_S_COL + PA_ROWS * (j & 1);
-#pragma unroll
-          for (uint32_t k = 0; k < 32; k++)
-            umma_bf16(d, a + (((k >> 2) * PA_KB + 32 * (k & 3)) >> 4),
-                      qd + (((k >> 2) * PA_QKB + 32 * (k & 3)) >> 4), id_s, k != 0);
-          umma_commit(&s.s_full[j & 1]);
-        }
-        __syncwarp();
-      };
-      logits(i);
+      // The next S^T waits for its tile, the next O^T step for its P; whichever is
+      // ready goes, the O^T step first (it frees a tile buffer).  In a fixed order
+      // one of them would hold up the other's input: with S^T first, filling a
+      // tile and multiplying took turns (5.1K instead of 3.0K cycles a tile).
+      const uint32_t end = i + n_tiles;
+      uint32_t js = i;  // next S^T; i: next O^T
+      const uint32_t begin = i;
+      long long t0 = clock64();
 #pragma unroll 1
-      for (int k = 0; k < n_tiles; k++, i++) {
-        if (k + 1 < n_tiles) logits(i + 1);  // while the softmax of tile i runs
-        if (!mbar_wait(&s.p_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
-        __syncwarp();
-        tc_fence_after();
-        // O^T += V^T P^T: four channel blocks, K = 64 keys in four steps
-        if (leader) {
-          const uint64_t a = vd + ((i & 1) * ((8 * PA_KB) >> 4));
-          const uint64_t b = pd + ((i & 1) * ((PA_KEYS * 128) >> 4));
+      while (i < end) {
+        if (i < js && mbar_test_warp(&s.p_full[i & 1], (i >> 1) & 1)) {
+          __syncwarp();
+          tc_fence_after();
+          // O^T += V^T P^T: four channel blocks, K = 64 keys in four steps
+          if (leader) {
+            const uint64_t a = vd + ((i & 1) * ((8 * PA_KB) >> 4));
+            const uint64_t b = pd + ((i & 1) * ((PA_KEYS * 128) >> 4));
 #pragma unroll
-          for (uint32_t j = 0; j < 16; j++)
-            umma_bf16(tmem + 64 * (j & 3), a + (((j & 3) * 2 * PA_KB + (j >> 2) * 2048) >> 4),
-                      b + (((j >> 2) * 2048) >> 4), id_o, k != 0 || j >= 4);
-          umma_commit(&s.empty[i & 1]);
+            for (uint32_t j = 0; j < 16; j++)
+              umma_bf16(tmem + 64 * (j & 3), a + (((j & 3) * 2 * PA_KB + (j >> 2) * 2048) >> 4),
+                        b + (((j >> 2) * 2048) >> 4), id_o, i != begin || j >= 4);
+            umma_commit(&s.empty[i & 1]);
+          }
+          i++;
+          t0 = clock64();
+        } else if (js < end && js < i + 2 && mbar_test_warp(&s.full[js & 1], (js >> 1) & 1)) {
+          __syncwarp();
+          tc_fence_after();
+          // S^T = K Q'^T: K = 512 in 32 steps
+          if (leader) {
+            const uint64_t a = kd + ((js & 1) * ((8 * PA_KB) >> 4));
+            const uint32_t d = tmem + PA_S_COL + PA_ROWS * (js & 1);
+#pragma unroll
+            for (uint32_t k = 0; k < 32; k++)
+              umma_bf16(d, a + (((k >> 2) * PA_KB + 32 * (k & 3)) >> 4),
+                        qd + (((k >> 2) * PA_QKB + 32 * (k & 3)) >> 4), id_s, k != 0);
+            umma_commit(&s.s_full[js & 1]);
+          }
+          js++;
+          t0 = clock64();
+        } else if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles || *(volatile int*)&s.abort)) {
+          s.abort = 1;  // nothing came: the other roles stop too
+          break;
         }
         __syncwarp();
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      i = end;
+      bar_sync<PA_RUN_NT>(BAR_RUN);
     }
   }
   if (s.abort && t == 0) set_status(p.status, ST_TIMEOUT);
