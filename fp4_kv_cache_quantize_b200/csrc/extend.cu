@@ -7,12 +7,14 @@
 // a whole, so every CTA that writes for a sequence first checks the sequence's
 // whole run; extend_commit_kernel makes the same check and advances counters.
 #include "csa2_internal.cuh"
+#include "umma_m64.cuh"
 #include "rope.cuh"
 
 namespace csa2 {
 
 constexpr int EX_NT = 256;
 constexpr int EX_LAYERS_PER_CTA = EX_NT / 64;
+constexpr int EX_FEW = 512;  // tokens up to which each has a CTA of its own
 
 // Tokens [lo, hi) of sequence b; false if the offsets are out of order or do
 // not start at 0.
@@ -73,7 +75,25 @@ __device__ __forceinline__ bool run_fits(const ExtendParams& p, int b, int count
   return ok;
 }
 
-// One CTA per token: part 0 packs the entry and projects its key (256 threads:
+// Eight channels of one window entry: rotated, E4M3, into its ring slot.
+__device__ __forceinline__ void window_row(const ExtendParams& p, int b, int l, int tok, int spos,
+                                           int ch) {
+  const float2* cs = p.rope_swa.table
+                         ? rope_row(p.rope_swa, p.pos ? __ldg(p.pos + tok) : spos, p.status)
+                         : nullptr;
+  float f[8];
+  rotated_chunk8(p.rope_swa, cs, p.x_swa + ((int64_t)l * p.total + tok) * CSA2_D, CSA2_D, ch, f);
+  uint32_t w2[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    w2[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE,
+                                               __NV_E4M3);
+  uint8_t* dst = p.swa + (((int64_t)l * p.batch + b) * CSA2_W + spos % CSA2_W) * CSA2_D + 8 * ch;
+  *reinterpret_cast<uint2*>(dst) = make_uint2((w2[0] & 0xFFFFu) | (w2[1] << 16),
+                                              (w2[2] & 0xFFFFu) | (w2[3] << 16));
+}
+
+// One CTA per token (few tokens): part 0 packs the entry and projects its key (256 threads:
 // 8 outputs x 16 channels each, partial sums reduced in a fixed order); parts
 // 1.. convert four layers' window entries each (64 threads per layer).
 __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams p) {
@@ -153,20 +173,264 @@ __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams 
 
   const int l = (blockIdx.y - (p.x ? 1 : 0)) * EX_LAYERS_PER_CTA + (t >> 6);
   if (l >= p.n_layers || tok < hi - CSA2_W) return;
-  const int spos = __ldg(p.swa_pos + b) + (tok - lo), ch = t & 63;
-  const float2* cs = p.rope_swa.table
-                         ? rope_row(p.rope_swa, p.pos ? __ldg(p.pos + tok) : spos, p.status)
-                         : nullptr;
-  float f[8];
-  rotated_chunk8(p.rope_swa, cs, p.x_swa + ((int64_t)l * p.total + tok) * CSA2_D, CSA2_D, ch, f);
-  uint32_t w2[4];
+  window_row(p, b, l, tok, __ldg(p.swa_pos + b) + (tok - lo), t & 63);
+}
+
+// ------------------------------------------------- many tokens: tiles of 64
+// One CTA per SM walks tiles of 64 tokens.  A warp reads four token rows straight
+// into registers (64 pieces of 8 channels each, two per lane: 512 consecutive
+// bytes per load, all of a tile's 64 KB in flight at once), packs the pieces in
+// front of the rotated channels and puts the raw rows into the swizzled tile
+// that the MMA reads: the key x W of 64 tokens is one tcgen05 product, M = 64,
+// N = 64, K = 512, W staying in shared memory.  Under the MMA, the rotated
+// channels are turned from the raw tile, all lanes busy whatever their share of
+// a row, and the next tile's rows are fetched.  Bound by memory: 1,024 + 416
+// bytes a token against 65,536 multiply-adds.
+constexpr int ET_NT = 512;
+constexpr int ET_TOK = 64;                              // tokens per tile: the MMA's M
+constexpr int ET_PER_WARP = ET_TOK / (ET_NT / 32);      // token rows per warp
+constexpr int ET_KB = ET_TOK * 128;                     // one 64-channel chunk of the tile
+
+struct EtSmem {
+  alignas(1024) uint8_t a[8 * ET_KB];        // raw bf16 rows: chunk kb, 64 rows of 128 B, swizzled
+  alignas(1024) uint8_t w[CSA2_D * 128];     // W: 512 rows (K) of 64 outputs, swizzled
+  int64_t row[ET_TOK];                       // pool row, -1: not written
+  int pos[ET_TOK];                           // rotation position
+  int seq_lo[2], seq_hi[2];                  // lowest and highest sequence of each 32 tokens
+  uint64_t mbar;
+  uint32_t tmem_base;
+};
+constexpr size_t ET_SMEM = sizeof(EtSmem) + 1024;
+
+__device__ __forceinline__ uint32_t et_at(int row, int piece) {
+  return (uint32_t)((piece >> 3) * ET_KB + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+
+// Packs the eight channels of a piece; lanes 2 j and 2 j + 1 hold one scale
+// group.  row < 0: nothing is written.
+__device__ __forceinline__ void et_pack(const ExtendParams& p, const float (&f)[8], int64_t row,
+                                        int piece) {
+  float amax = amax8(f);
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  uint8_t sb;
+  const uint32_t packed = fp4_encode8(f, amax, &sb);
+  if (row < 0) return;
+  reinterpret_cast<uint32_t*>(p.codes + row * (CSA2_D / 2))[piece] = packed;
+  if ((piece & 1) == 0) p.scales[row * (CSA2_D / 16) + (piece >> 1)] = sb;
+}
+
+__global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  EtSmem& s = *reinterpret_cast<EtSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~uintptr_t(1023));
+  const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
+  const int n_tiles = (p.total + ET_TOK - 1) / ET_TOK;
+  pdl_launch_dependents();
+  if (t == 0) {
+    mbar_init(&s.mbar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s.tmem_base, 64);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  for (int i = t; i < CSA2_D * 8; i += ET_NT)
+    cp_async16(s.w + (i >> 3) * 128 + (((i & 7) ^ ((i >> 3) & 7)) << 4),
+               reinterpret_cast<const uint8_t*>(p.w_idx) + 16 * i);
+  cp_async_commit();
+
+  uint4 v[ET_PER_WARP][2];
+  auto fetch = [&](int tile) {
 #pragma unroll
-  for (int k = 0; k < 4; k++)
-    w2[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE,
-                                               __NV_E4M3);
-  uint8_t* dst = p.swa + (((int64_t)l * p.batch + b) * CSA2_W + spos % CSA2_W) * CSA2_D + 8 * ch;
-  *reinterpret_cast<uint2*>(dst) = make_uint2((w2[0] & 0xFFFFu) | (w2[1] << 16),
-                                              (w2[2] & 0xFFFFu) | (w2[3] << 16));
+    for (int k = 0; k < ET_PER_WARP; k++) {
+      const int tok = tile * ET_TOK + warp * ET_PER_WARP + k;
+      const uint4* x = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * CSA2_D) + lane;
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        v[k][h] = tok < p.total ? __ldg(x + 32 * h) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  fetch(blockIdx.x);
+  const int turned = p.rope.table ? p.rope.dims : 0;  // rotated channels, at the end of a row
+  const int plain = (CSA2_D - turned) / 8;            // pieces in front of them (even)
+  uint32_t phase = 0;
+  bool alive = true;
+  for (int tile = blockIdx.x; tile < n_tiles && alive; tile += gridDim.x) {
+    // ---- the tokens' sequences, rows and positions
+    const int tok0 = tile * ET_TOK, n = min(ET_TOK, p.total - tok0);
+    if (t < ET_TOK) {
+      int seq = -1;
+      int64_t row = -1;
+      int pos = 0;
+      if (t < n) {
+        seq = seq_of(p, tok0 + t);
+        int lo, hi;
+        if (seq >= 0 && run_of(p, seq, lo, hi)) {
+          const int64_t at = (int64_t)p.n_rows[seq] + (tok0 + t - lo);
+          if (at >= 0) row = extend_row(p, seq, at);
+          pos = p.pos ? __ldg(p.pos + tok0 + t) : (int)at;
+        }
+      }
+      s.row[t] = row;
+      s.pos[t] = pos;
+      const int a = __reduce_min_sync(0xffffffffu, seq < 0 ? p.batch : seq);
+      const int z = __reduce_max_sync(0xffffffffu, seq);
+      if (lane == 0) {
+        s.seq_lo[warp] = a;
+        s.seq_hi[warp] = z;
+      }
+    }
+    __syncthreads();
+    // a run that does not fit is not written at all: a warp per sequence checks
+    // all of its pages (none where every token lies behind the last run: then the
+    // range is [batch, -1])
+    const int seq_hi = max(s.seq_hi[0], s.seq_hi[1]);
+    for (int b = min(s.seq_lo[0], s.seq_lo[1]) + warp; b <= seq_hi; b += ET_NT / 32) {
+      int lo, hi;
+      if (!run_of(p, b, lo, hi) || lo == hi) continue;
+      if (!__all_sync(0xffffffffu, run_fits(p, b, hi - lo, lane, 32)))
+        for (int k = max(lo - tok0, 0) + lane; k < min(hi - tok0, ET_TOK); k += 32) s.row[k] = -1;
+    }
+    __syncthreads();
+    // ---- pack what is not rotated; raw rows into the tile
+#pragma unroll
+    for (int k = 0; k < ET_PER_WARP; k++) {
+      const int r = warp * ET_PER_WARP + k;
+      const int64_t row = s.row[r];
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int piece = 32 * h + lane;
+        *reinterpret_cast<uint4*>(s.a + et_at(r, piece)) = v[k][h];
+        if (32 * h < plain) {
+          float f[8];
+          unpack_bf16x8(v[k][h], f);
+          et_pack(p, f, piece < plain ? row : -1, piece);
+        }
+      }
+    }
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t da = sdesc_k128(smem_u32(s.a)), db = sdesc_mn128(smem_u32(s.w), 65536, 1024);
+        constexpr uint32_t id = idesc_bf16_f32(ET_TOK, CSA2_DI) | (1u << 16);  // W is read MN-major
+#pragma unroll
+        for (uint32_t k = 0; k < 32; k++)
+          umma_bf16(s.tmem_base, da + (((k >> 2) * ET_KB + 32 * (k & 3)) >> 4), db + ((k * 2048) >> 4),
+                    id, k != 0);
+        umma_commit(&s.mbar);
+      }
+      __syncwarp();
+    }
+    if (tile + (int)gridDim.x < n_tiles) fetch(tile + gridDim.x);
+    // ---- the rotated pieces, from the raw tile
+    const int per = 64 - plain;
+    for (int i = t; i < ET_TOK * per; i += ET_NT) {  // (whole warps: 64 * per is a multiple of 32)
+      const int r = i / per, piece = plain + i - r * per, k = 8 * (piece - plain);
+      float f[8];
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(s.a + et_at(r, piece)), f);
+      const float2* cs = rope_row(p.rope, s.pos[r], p.status);
+      if (p.rope.style == CSA2_ROPE_PAIRS) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const float2 y = rotate_pair(f[2 * j], f[2 * j + 1], __ldg(cs + k / 2 + j));
+          f[2 * j] = round_bf16(y.x);
+          f[2 * j + 1] = round_bf16(y.y);
+        }
+      } else {
+        const int half = p.rope.dims / 2;
+        const bool first = k < half;
+        float g[8];
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(s.a + et_at(r, piece + (first ? half : -half) / 8)), g);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float2 c = __ldg(cs + (first ? k : k - half) + j);
+          const float2 y = first ? rotate_pair(f[j], g[j], c) : rotate_pair(g[j], f[j], c);
+          f[j] = round_bf16(first ? y.x : y.y);
+        }
+      }
+      et_pack(p, f, s.row[r], piece);
+    }
+    // ---- the keys: rotate the sums, round once
+    const bool ok = mbar_wait(&s.mbar, phase, nullptr);
+    phase ^= 1;
+    __syncwarp();
+    tc_fence_after();
+    if (warp < 4 && ok) {
+      uint32_t acc[32];
+      tmem_ld_16x256b_x4(s.tmem_base + ((uint32_t)(32 * warp) << 16), *reinterpret_cast<uint32_t(*)[16]>(acc));
+      tmem_ld_16x256b_x4(s.tmem_base + ((uint32_t)(32 * warp) << 16) + 32,
+                         *reinterpret_cast<uint32_t(*)[16]>(acc + 16));
+      tmem_ld_wait();
+      const int rk = p.rope_idx.table ? p.rope_idx.dims : 0;  // 0, 32 or 64
+#pragma unroll
+      for (int h = 0; h < 2; h++) {  // rows lane / 4 and lane / 4 + 8 of the warp's 16
+        const int r = 16 * warp + (lane >> 2) + 8 * h;
+        const int64_t row = s.row[r];
+        if (row < 0) continue;
+        float2 y[8];  // columns 8 n + 2 (lane % 4) + {0, 1}
+#pragma unroll
+        for (int nn = 0; nn < 8; nn++)
+          y[nn] = make_float2(__uint_as_float(acc[4 * nn + 2 * h]), __uint_as_float(acc[4 * nn + 2 * h + 1]));
+        if (rk) {
+          const float2* cs = rope_row(p.rope_idx, s.pos[r], p.status);
+          if (p.rope_idx.style == CSA2_ROPE_PAIRS) {
+#pragma unroll
+            for (int nn = 0; nn < 8; nn++)
+              if (8 * nn >= CSA2_DI - rk)
+                y[nn] = rotate_pair(y[nn].x, y[nn].y,
+                                    __ldg(cs + 4 * nn + (lane & 3) - (CSA2_DI - rk) / 2));
+          } else {
+#pragma unroll
+            for (int nn = 0; nn < 8; nn++) {  // the pair's first channel is in column block nn
+              const int c = 8 * nn - (CSA2_DI - rk);
+              if (c < 0 || c >= rk / 2) continue;
+              const float2* a = cs + c + 2 * (lane & 3);
+              // its second lies rk / 16 blocks on
+              float2& z = rk == 64 ? y[(nn + 4) & 7] : y[(nn + 2) & 7];
+              const float2 u = rotate_pair(y[nn].x, z.x, __ldg(a));
+              const float2 w = rotate_pair(y[nn].y, z.y, __ldg(a + 1));
+              y[nn] = make_float2(u.x, w.x);
+              z = make_float2(u.y, w.y);
+            }
+          }
+        }
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.idx_k + row * CSA2_DI) + (lane & 3);
+#pragma unroll
+        for (int nn = 0; nn < 8; nn++) dst[4 * nn] = pack_bf16x2(y[nn].x, y[nn].y);
+      }
+    }
+    tc_fence_before();
+    alive = __syncthreads_and(ok);
+    tc_fence_after();
+  }
+  if (!alive && t == 0) set_status(p.status, ST_TIMEOUT);
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(s.tmem_base, 64);
+}
+
+// The window entries of many tokens: one CTA per 16 of the last 128 tokens of a
+// sequence's run and layer, 64 threads per row.
+constexpr int EW_TOK = 16;
+__global__ void __launch_bounds__(EX_NT) extend_window_kernel(const ExtendParams p) {
+  const int t = threadIdx.x, b = blockIdx.x / (CSA2_W / EW_TOK), part = blockIdx.x % (CSA2_W / EW_TOK);
+  const int l = blockIdx.y, ch = t & 63;
+  pdl_launch_dependents();
+  pdl_wait();
+  int lo, hi;
+  if (!run_of(p, b, lo, hi)) return;
+  const int last = hi - part * EW_TOK, first = max(lo, last - EW_TOK);
+  if (last <= lo) return;
+  if (!__syncthreads_and(run_fits(p, b, hi - lo, t, EX_NT))) return;
+  const int spos0 = __ldg(p.swa_pos + b);
+  for (int tok = first + (t >> 6); tok < last; tok += EX_NT / 64) {
+    const int spos = spos0 + (tok - lo);
+    window_row(p, b, l, tok, spos, ch);
+  }
 }
 
 // Advances the counters once every write of the step has landed: one warp per
@@ -201,12 +465,35 @@ cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (p.total > 0) {
+  if (p.total <= EX_FEW) {
     cfg.gridDim = dim3(p.total, (p.x ? 1 : 0) +
                                     (p.n_layers + EX_LAYERS_PER_CTA - 1) / EX_LAYERS_PER_CTA);
     trace_mark("extend", st);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, extend_token_kernel, p);
     if (e != cudaSuccess) return e;
+  } else {
+    if (p.x) {
+      static PerDeviceOnce attr;
+      cudaError_t e = attr.run([](int&) {
+        return cudaFuncSetAttribute(extend_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)ET_SMEM);
+      });
+      if (e != cudaSuccess) return e;
+      const int tiles = (p.total + ET_TOK - 1) / ET_TOK, sms = num_sms();
+      cfg.gridDim = dim3(tiles < sms ? tiles : sms);
+      cfg.blockDim = dim3(ET_NT);
+      cfg.dynamicSmemBytes = ET_SMEM;
+      trace_mark("extend", st);
+      if ((e = cudaLaunchKernelEx(&cfg, extend_tile_kernel, p)) != cudaSuccess) return e;
+      cfg.blockDim = dim3(EX_NT);
+      cfg.dynamicSmemBytes = 0;
+    }
+    if (p.n_layers > 0) {
+      cfg.gridDim = dim3(p.batch * (CSA2_W / EW_TOK), p.n_layers);
+      trace_mark("extend_window", st);
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, extend_window_kernel, p);
+      if (e != cudaSuccess) return e;
+    }
   }
   cfg.gridDim = dim3((p.batch * 32 + EX_NT - 1) / EX_NT);
   trace_mark("extend_commit", st);

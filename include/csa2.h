@@ -440,7 +440,7 @@ csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32
  * unmapped page, a negative counter, token offsets out of order or beyond
  * total) is left unchanged as a whole, rows, windows and counters, and
  * CSA2_ERR_DEVICE_CHECK is recorded.  ws: at least CSA2_WS_HEADER bytes.
- * Two launches; asynchronous on stream.
+ * Two or three launches; asynchronous on stream.
  */
 typedef struct {
   csa2_kv_view kv;

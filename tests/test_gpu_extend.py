@@ -206,6 +206,10 @@ class Case:
     ([40, 200], [5, 0], dict(dims=0, idx_dims=64, L=1)),
     ([129, 127, 128], [0, 0, 0], dict(dims=32, idx_dims=0, entries=False)),
     ([700, 1], [123, 77], dict(dims=64, idx_dims=64, L=1, tail=50)),
+    ([513], [0], dict(dims=512, idx_dims=64, L=0, pos="given")),
+    ([1, 0, 1500, 63, 64, 65, 0, 0, 2], [64, 9, 100, 0, 1, 63, 5, 0, 200], dict(dims=32, idx_dims=32, tail=70)),
+    ([0, 0, 900, 0], [0, 1, 2, 3], dict(dims=0, idx_dims=0, pos="given", tail=1)),
+    ([600, 300], [5, 0], dict(dims=96, idx_dims=0, entries=False, L=3)),
 ])
 def test_extend(lib, orc, counts, n0, kw, paged, halves):
     c = Case(lib, orc, counts, n0, paged=paged, halves=halves, **kw)
@@ -241,11 +245,14 @@ def test_extend_far_position_of_a_long_cache(lib, orc):
     c.check()
 
 
+@pytest.mark.parametrize("many", [0, 700])
 @pytest.mark.parametrize("what", ["unmapped", "page_out_of_pool", "capacity", "negative_rows", "negative_window",
                                   "offsets"])
-def test_extend_refuses_a_run_as_a_whole(lib, orc, what):
-    """The sequence stays as it was, the others are extended."""
-    c = Case(lib, orc, [10, 200, 5], [60, 30, 3], paged=what != "capacity", L=1)
+def test_extend_refuses_a_run_as_a_whole(lib, orc, what, many):
+    """The sequence stays as it was, the others are extended (few tokens, and
+    many)."""
+    counts = [10 + many, 200, 5]
+    c = Case(lib, orc, counts, [60, 30, 3], paged=what != "capacity", L=1)
     d, bad = c.d, 1
     if what == "unmapped":
         c.page_table[1, 2] = d["page_table"][1, 2] = -1
@@ -259,7 +266,7 @@ def test_extend_refuses_a_run_as_a_whole(lib, orc, what):
     elif what == "negative_window":
         c.swa_pos[1] = d["swa_pos"][1] = -7
     else:  # the last run would end behind the tokens
-        c.cu[3] = d["cu"][3] = 216
+        c.cu[3] = d["cu"][3] = sum(counts) + 1
         bad = 2
     # rotation positions stay those that the case was made with
     d["pos"] = torch.cat([c.at, torch.zeros(c.T - len(c.at), dtype=torch.int32)]).cuda()
