@@ -177,27 +177,33 @@ __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams 
 }
 
 // ------------------------------------------------- many tokens: tiles of 64
-// One CTA per SM walks tiles of 64 tokens.  A warp reads four token rows straight
-// into registers (64 pieces of 8 channels each, two per lane: 512 consecutive
-// bytes per load, all of a tile's 64 KB in flight at once), packs the pieces in
-// front of the rotated channels and puts the raw rows into the swizzled tile
-// that the MMA reads: the key x W of 64 tokens is one tcgen05 product, M = 64,
-// N = 64, K = 512, W staying in shared memory.  Under the MMA, the rotated
-// channels are turned from the raw tile, all lanes busy whatever their share of
-// a row, and the next tile's rows are fetched.  Bound by memory: 1,024 + 416
-// bytes a token against 65,536 multiply-adds.
-constexpr int ET_NT = 512;
-constexpr int ET_TOK = 64;                              // tokens per tile: the MMA's M
-constexpr int ET_PER_WARP = ET_TOK / (ET_NT / 32);      // token rows per warp
+// One CTA per SM, two groups of eight warps that each walk tiles of 64 tokens.
+// cp.async brings a tile's raw rows into the swizzled layout that the MMA reads:
+// the key x W of 64 tokens is one tcgen05 product, M = 64, N = 64, K = 512, with
+// one W in shared memory for both groups.  Under it the rows are packed from the
+// same tile, first the pieces (8 channels) in front of the rotated ones, then the
+// rotated ones, all lanes busy whatever their share of a row, in loops short
+// enough to stay in the instruction cache.  Memory would allow 1,440 bytes a
+// token at its rate; what bounds a tile are its dependent phases (rows, packing,
+// turning, keys), which is why two groups take turns on the SM's issue slots.
+// With few tokens the tiles are shorter (32 or 16, the product's other rows
+// idle), so that every SM has some.
+constexpr int ET_GROUPS = 2;
+constexpr int ET_GT = 256;                              // threads of a group
+constexpr int ET_NT = ET_GROUPS * ET_GT;
+constexpr int ET_TOK = 64;                              // most tokens of a tile: the MMA's M
 constexpr int ET_KB = ET_TOK * 128;                     // one 64-channel chunk of the tile
 
-struct EtSmem {
-  alignas(1024) uint8_t a[8 * ET_KB];        // raw bf16 rows: chunk kb, 64 rows of 128 B, swizzled
-  alignas(1024) uint8_t w[CSA2_D * 128];     // W: 512 rows (K) of 64 outputs, swizzled
-  int64_t row[ET_TOK];                       // pool row, -1: not written
-  int pos[ET_TOK];                           // rotation position
+struct EtGroup {
+  int64_t row[2][ET_TOK];                    // by tile parity: pool row, -1: not written
+  int pos[2][ET_TOK];                        // rotation position
   int seq_lo[2], seq_hi[2];                  // lowest and highest sequence of each 32 tokens
   uint64_t mbar;
+};
+struct EtSmem {
+  alignas(1024) uint8_t a[ET_GROUPS][8 * ET_KB];  // raw bf16 rows: chunk kb, 64 rows of 128 B, swizzled
+  alignas(1024) uint8_t w[CSA2_D * 128];          // W: 512 rows (K) of 64 outputs, swizzled
+  EtGroup g[ET_GROUPS];
   uint32_t tmem_base;
 };
 constexpr size_t ET_SMEM = sizeof(EtSmem) + 1024;
@@ -219,198 +225,250 @@ __device__ __forceinline__ void et_pack(const ExtendParams& p, const float (&f)[
   if ((piece & 1) == 0) p.scales[row * (CSA2_D / 16) + (piece >> 1)] = sb;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* a) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
+// The table row of a position that a later step reads (clamped alike).
+__device__ __forceinline__ void prefetch_rope(const RopeParams& r, int pos) {
+  if (r.table == nullptr) return;
+  pos = min(max(pos, 0), r.n_pos - 1);
+  const char* a = reinterpret_cast<const char*>(r.table + (int64_t)pos * (r.dims / 2));
+  for (int i = 0; i < r.dims * 4; i += 128) prefetch_l2(a + i);
+}
+
+// The rows and positions of a tile's tokens (threads 0..63 of the group).
+__device__ __forceinline__ void et_places(const ExtendParams& p, EtGroup& g, int tile, int buf,
+                                          int t) {
+  const int tok = tile * p.tile + t;
+  int seq = -1, pos = 0;
+  int64_t row = -1;
+  if (t < p.tile && tok < p.total) {
+    const char* x = reinterpret_cast<const char*>(p.x + (int64_t)tok * CSA2_D);
+    for (int i = 0; i < CSA2_D * 2; i += 128) prefetch_l2(x + i);
+    seq = seq_of(p, tok);
+    int lo, hi;
+    if (seq >= 0 && run_of(p, seq, lo, hi)) {
+      const int64_t at = (int64_t)p.n_rows[seq] + (tok - lo);
+      if (at >= 0) row = extend_row(p, seq, at);
+      pos = p.pos ? __ldg(p.pos + tok) : (int)at;
+      prefetch_rope(p.rope, pos);
+      prefetch_rope(p.rope_idx, pos);
+    }
+  }
+  g.row[buf][t] = row;
+  g.pos[buf][t] = pos;
+  const int a = __reduce_min_sync(0xffffffffu, seq < 0 ? p.batch : seq);
+  const int z = __reduce_max_sync(0xffffffffu, seq);
+  if ((t & 31) == 0) {
+    g.seq_lo[t >> 5] = a;
+    g.seq_hi[t >> 5] = z;
+  }
+}
+
+// A run that does not fit is not written at all: a warp per sequence of the tile
+// checks all of its pages (none where every token lies behind the last run: then
+// the range is [batch, -1]).
+__device__ __forceinline__ void et_check(const ExtendParams& p, EtGroup& g, int tile, int buf,
+                                         int warp, int lane) {
+  const int tok0 = tile * p.tile, seq_hi = max(g.seq_hi[0], g.seq_hi[1]);
+  for (int b = min(g.seq_lo[0], g.seq_lo[1]) + warp; b <= seq_hi; b += ET_GT / 32) {
+    int lo, hi;
+    if (!run_of(p, b, lo, hi) || lo == hi) continue;
+    if (!__all_sync(0xffffffffu, run_fits(p, b, hi - lo, lane, 32)))
+      for (int k = max(lo - tok0, 0) + lane; k < min(hi - tok0, p.tile); k += 32)
+        g.row[buf][k] = -1;
+  }
+}
+
+// The pieces in front of the rotated ones, packed.
+__device__ __forceinline__ void et_plain(const ExtendParams& p, const uint8_t* a, const EtGroup& g,
+                                         int buf, int plain, int t) {
+#pragma unroll 2
+  for (int i = t; i < p.tile * plain; i += ET_GT) {  // (whole warps: a multiple of 16 * 4)
+    const int r = i / plain, piece = i - r * plain;
+    float f[8];
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(a + et_at(r, piece)), f);
+    et_pack(p, f, g.row[buf][r], piece);
+  }
+}
+
+// The rotated pieces of a tile, turned from the raw rows and packed.
+__device__ __forceinline__ void et_turn(const ExtendParams& p, const uint8_t* a, const EtGroup& g,
+                                        int buf, int plain, int t) {
+  const int per = 64 - plain;
+  for (int i = t; i < p.tile * per; i += ET_GT) {  // (whole warps: a multiple of 16 * 4)
+    const int r = i / per, piece = plain + i - r * per, k = 8 * (piece - plain);
+    float f[8];
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(a + et_at(r, piece)), f);
+    const float2* cs = rope_row(p.rope, g.pos[buf][r], p.status);
+    if (p.rope.style == CSA2_ROPE_PAIRS) {
+      const float4* c4 = reinterpret_cast<const float4*>(cs + k / 2);
+      const float4 c[2] = {__ldg(c4), __ldg(c4 + 1)};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const float2 y = rotate_pair(f[2 * j], f[2 * j + 1],
+                                     (j & 1) ? make_float2(c[j >> 1].z, c[j >> 1].w)
+                                             : make_float2(c[j >> 1].x, c[j >> 1].y));
+        f[2 * j] = round_bf16(y.x);
+        f[2 * j + 1] = round_bf16(y.y);
+      }
+    } else {
+      const int half = p.rope.dims / 2;
+      const bool first = k < half;
+      float h[8];
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(a + et_at(r, piece + (first ? half : -half) / 8)), h);
+      const float4* c4 = reinterpret_cast<const float4*>(cs + (first ? k : k - half));
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const float4 c = __ldg(c4 + j);
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float2 cc = e ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
+          float& fj = f[2 * j + e];
+          const float2 y = first ? rotate_pair(fj, h[2 * j + e], cc) : rotate_pair(h[2 * j + e], fj, cc);
+          fj = round_bf16(first ? y.x : y.y);
+        }
+      }
+    }
+    et_pack(p, f, g.row[buf][r], piece);
+  }
+}
+
+// The keys of a tile: the sums rotated in fp64, rounded once.  Warp (quad, part):
+// tokens 16 quad + lane / 4 and + 8, column blocks of 8 that hold whole pairs.
+__device__ __forceinline__ void et_keys(const ExtendParams& p, const EtGroup& g, int buf,
+                                        uint32_t tmem, int warp, int lane) {
+  const int quad = warp & 3, part = warp >> 2;
+  const int rk = p.rope_idx.table ? p.rope_idx.dims : 0;  // 0, 32 or 64
+  const bool halves = rk && p.rope_idx.style == CSA2_ROPE_HALVES;
+  // blocks 2 part, 2 part + 1, + 4, + 5: with HALVES of 64 block n pairs with n +
+  // 4; of 32, blocks 4, 5 pair with 6, 7: part 0 takes 0..3 then, part 1 the rest
+  const int b0 = halves && rk == 32 ? 4 * part : 2 * part, up = halves && rk == 32 ? 2 : 4;
+  uint32_t acc[4][4];
+#pragma unroll
+  for (int n = 0; n < 4; n++)
+    tmem_ld_16x256b_x1(tmem + ((uint32_t)(32 * quad) << 16) + 8 * (b0 + (n & 1) + (n >> 1) * up), acc[n]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int r = 16 * quad + (lane >> 2) + 8 * h;
+    const int64_t row = g.row[buf][r];
+    if (row < 0) continue;
+    float2 y[4];  // block n: columns 8 block + 2 (lane % 4) + {0, 1}
+#pragma unroll
+    for (int n = 0; n < 4; n++)
+      y[n] = make_float2(__uint_as_float(acc[n][2 * h]), __uint_as_float(acc[n][2 * h + 1]));
+    if (rk) {
+      const float2* cs = rope_row(p.rope_idx, g.pos[buf][r], p.status);
+      if (!halves) {
+#pragma unroll
+        for (int n = 0; n < 4; n++) {
+          const int c = 8 * (b0 + (n & 1) + (n >> 1) * up) - (CSA2_DI - rk);
+          if (c >= 0) y[n] = rotate_pair(y[n].x, y[n].y, __ldg(cs + c / 2 + (lane & 3)));
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+          const int c = 8 * (b0 + n) - (CSA2_DI - rk);
+          if (c < 0) continue;  // (dims 32, part 0: nothing is rotated)
+          const float4 a = __ldg(reinterpret_cast<const float4*>(cs + c) + (lane & 3));
+          const float2 u = rotate_pair(y[n].x, y[n + 2].x, make_float2(a.x, a.y));
+          const float2 w = rotate_pair(y[n].y, y[n + 2].y, make_float2(a.z, a.w));
+          y[n] = make_float2(u.x, w.x);
+          y[n + 2] = make_float2(u.y, w.y);
+        }
+      }
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.idx_k + row * CSA2_DI) + (lane & 3);
+#pragma unroll
+    for (int n = 0; n < 4; n++)
+      dst[4 * (b0 + (n & 1) + (n >> 1) * up)] = pack_bf16x2(y[n].x, y[n].y);
+  }
+}
+
 __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParams p) {
   extern __shared__ uint8_t smem_raw[];
   EtSmem& s = *reinterpret_cast<EtSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
-  const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
-  const int n_tiles = (p.total + ET_TOK - 1) / ET_TOK;
+  const int grp = __shfl_sync(0xffffffffu, threadIdx.x / ET_GT, 0);
+  const int t = threadIdx.x % ET_GT, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
+  const int n_tiles = (p.total + p.tile - 1) / p.tile, step = gridDim.x * ET_GROUPS;
+  EtGroup& g = s.g[grp];
+  uint8_t* const a = s.a[grp];
   pdl_launch_dependents();
   if (t == 0) {
-    mbar_init(&s.mbar, 1);
+    mbar_init(&g.mbar, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {
-    tmem_alloc(&s.tmem_base, 64);
+  if (threadIdx.x < 32) {
+    tmem_alloc(&s.tmem_base, 64 * ET_GROUPS);
     tmem_relinquish();
   }
   pdl_wait();
-  for (int i = t; i < CSA2_D * 8; i += ET_NT)
+  for (int i = threadIdx.x; i < CSA2_D * 8; i += ET_NT)
     cp_async16(s.w + (i >> 3) * 128 + (((i & 7) ^ ((i >> 3) & 7)) << 4),
                reinterpret_cast<const uint8_t*>(p.w_idx) + 16 * i);
   cp_async_commit();
 
-  uint4 v[ET_PER_WARP][2];
-  auto fetch = [&](int tile) {
-#pragma unroll
-    for (int k = 0; k < ET_PER_WARP; k++) {
-      const int tok = tile * ET_TOK + warp * ET_PER_WARP + k;
-      const uint4* x = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * CSA2_D) + lane;
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        v[k][h] = tok < p.total ? __ldg(x + 32 * h) : make_uint4(0u, 0u, 0u, 0u);
-    }
+  auto fetch = [&](int tile) {  // the tile's rows (those behind the last token: any)
+    const int n = min(p.tile, p.total - tile * p.tile) * 64;
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x + (int64_t)tile * p.tile * CSA2_D);
+    for (int i = t; i < n; i += ET_GT) cp_async16(a + et_at(i >> 6, i & 63), x + 16 * i);
+    cp_async_commit();
   };
-  fetch(blockIdx.x);
+  // neighbouring tiles go to different CTAs: few tiles spread over all SMs
+  int tile = blockIdx.x + grp * gridDim.x;
+  fetch(tile);
+  if (warp < 2) et_places(p, g, tile, 0, t);
+  cp_async_wait_all();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();  // W, the tensor memory's base, the first places
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base + 64 * grp;
+  et_check(p, g, tile, 0, warp, lane);
   const int turned = p.rope.table ? p.rope.dims : 0;  // rotated channels, at the end of a row
   const int plain = (CSA2_D - turned) / 8;            // pieces in front of them (even)
-  uint32_t phase = 0;
   bool alive = true;
-  for (int tile = blockIdx.x; tile < n_tiles && alive; tile += gridDim.x) {
-    // ---- the tokens' sequences, rows and positions
-    const int tok0 = tile * ET_TOK, n = min(ET_TOK, p.total - tok0);
-    if (t < ET_TOK) {
-      int seq = -1;
-      int64_t row = -1;
-      int pos = 0;
-      if (t < n) {
-        seq = seq_of(p, tok0 + t);
-        int lo, hi;
-        if (seq >= 0 && run_of(p, seq, lo, hi)) {
-          const int64_t at = (int64_t)p.n_rows[seq] + (tok0 + t - lo);
-          if (at >= 0) row = extend_row(p, seq, at);
-          pos = p.pos ? __ldg(p.pos + tok0 + t) : (int)at;
-        }
-      }
-      s.row[t] = row;
-      s.pos[t] = pos;
-      const int a = __reduce_min_sync(0xffffffffu, seq < 0 ? p.batch : seq);
-      const int z = __reduce_max_sync(0xffffffffu, seq);
-      if (lane == 0) {
-        s.seq_lo[warp] = a;
-        s.seq_hi[warp] = z;
-      }
-    }
-    __syncthreads();
-    // a run that does not fit is not written at all: a warp per sequence checks
-    // all of its pages (none where every token lies behind the last run: then the
-    // range is [batch, -1])
-    const int seq_hi = max(s.seq_hi[0], s.seq_hi[1]);
-    for (int b = min(s.seq_lo[0], s.seq_lo[1]) + warp; b <= seq_hi; b += ET_NT / 32) {
-      int lo, hi;
-      if (!run_of(p, b, lo, hi) || lo == hi) continue;
-      if (!__all_sync(0xffffffffu, run_fits(p, b, hi - lo, lane, 32)))
-        for (int k = max(lo - tok0, 0) + lane; k < min(hi - tok0, ET_TOK); k += 32) s.row[k] = -1;
-    }
-    __syncthreads();
-    // ---- pack what is not rotated; raw rows into the tile
-#pragma unroll
-    for (int k = 0; k < ET_PER_WARP; k++) {
-      const int r = warp * ET_PER_WARP + k;
-      const int64_t row = s.row[r];
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int piece = 32 * h + lane;
-        *reinterpret_cast<uint4*>(s.a + et_at(r, piece)) = v[k][h];
-        if (32 * h < plain) {
-          float f[8];
-          unpack_bf16x8(v[k][h], f);
-          et_pack(p, f, piece < plain ? row : -1, piece);
-        }
-      }
-    }
-    cp_async_wait_all();
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
+  bar_sync<ET_GT>(1 + grp);
+  for (uint32_t n = 0; tile < n_tiles && alive; tile += step, n++) {
+    const int buf = n & 1;
     if (warp == 0) {
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t da = sdesc_k128(smem_u32(s.a)), db = sdesc_mn128(smem_u32(s.w), 65536, 1024);
+        const uint64_t da = sdesc_k128(smem_u32(a)), db = sdesc_mn128(smem_u32(s.w), 65536, 1024);
         constexpr uint32_t id = idesc_bf16_f32(ET_TOK, CSA2_DI) | (1u << 16);  // W is read MN-major
 #pragma unroll
         for (uint32_t k = 0; k < 32; k++)
-          umma_bf16(s.tmem_base, da + (((k >> 2) * ET_KB + 32 * (k & 3)) >> 4), db + ((k * 2048) >> 4),
-                    id, k != 0);
-        umma_commit(&s.mbar);
+          umma_bf16(tmem, da + (((k >> 2) * ET_KB + 32 * (k & 3)) >> 4), db + ((k * 2048) >> 4), id,
+                    k != 0);
+        umma_commit(&g.mbar);
       }
       __syncwarp();
     }
-    if (tile + (int)gridDim.x < n_tiles) fetch(tile + gridDim.x);
-    // ---- the rotated pieces, from the raw tile
-    const int per = 64 - plain;
-    for (int i = t; i < ET_TOK * per; i += ET_NT) {  // (whole warps: 64 * per is a multiple of 32)
-      const int r = i / per, piece = plain + i - r * per, k = 8 * (piece - plain);
-      float f[8];
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(s.a + et_at(r, piece)), f);
-      const float2* cs = rope_row(p.rope, s.pos[r], p.status);
-      if (p.rope.style == CSA2_ROPE_PAIRS) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const float2 y = rotate_pair(f[2 * j], f[2 * j + 1], __ldg(cs + k / 2 + j));
-          f[2 * j] = round_bf16(y.x);
-          f[2 * j + 1] = round_bf16(y.y);
-        }
-      } else {
-        const int half = p.rope.dims / 2;
-        const bool first = k < half;
-        float g[8];
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(s.a + et_at(r, piece + (first ? half : -half) / 8)), g);
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-          const float2 c = __ldg(cs + (first ? k : k - half) + j);
-          const float2 y = first ? rotate_pair(f[j], g[j], c) : rotate_pair(g[j], f[j], c);
-          f[j] = round_bf16(first ? y.x : y.y);
-        }
-      }
-      et_pack(p, f, s.row[r], piece);
-    }
-    // ---- the keys: rotate the sums, round once
-    const bool ok = mbar_wait(&s.mbar, phase, nullptr);
-    phase ^= 1;
+    const bool more = tile + step < n_tiles;
+    if (more && warp < 2) et_places(p, g, tile + step, buf ^ 1, t);
+    et_plain(p, a, g, buf, plain, t);
+    et_turn(p, a, g, buf, plain, t);
+    const bool ok = mbar_wait(&g.mbar, n & 1, nullptr);
     __syncwarp();
     tc_fence_after();
-    if (warp < 4 && ok) {
-      uint32_t acc[32];
-      tmem_ld_16x256b_x4(s.tmem_base + ((uint32_t)(32 * warp) << 16), *reinterpret_cast<uint32_t(*)[16]>(acc));
-      tmem_ld_16x256b_x4(s.tmem_base + ((uint32_t)(32 * warp) << 16) + 32,
-                         *reinterpret_cast<uint32_t(*)[16]>(acc + 16));
-      tmem_ld_wait();
-      const int rk = p.rope_idx.table ? p.rope_idx.dims : 0;  // 0, 32 or 64
-#pragma unroll
-      for (int h = 0; h < 2; h++) {  // rows lane / 4 and lane / 4 + 8 of the warp's 16
-        const int r = 16 * warp + (lane >> 2) + 8 * h;
-        const int64_t row = s.row[r];
-        if (row < 0) continue;
-        float2 y[8];  // columns 8 n + 2 (lane % 4) + {0, 1}
-#pragma unroll
-        for (int nn = 0; nn < 8; nn++)
-          y[nn] = make_float2(__uint_as_float(acc[4 * nn + 2 * h]), __uint_as_float(acc[4 * nn + 2 * h + 1]));
-        if (rk) {
-          const float2* cs = rope_row(p.rope_idx, s.pos[r], p.status);
-          if (p.rope_idx.style == CSA2_ROPE_PAIRS) {
-#pragma unroll
-            for (int nn = 0; nn < 8; nn++)
-              if (8 * nn >= CSA2_DI - rk)
-                y[nn] = rotate_pair(y[nn].x, y[nn].y,
-                                    __ldg(cs + 4 * nn + (lane & 3) - (CSA2_DI - rk) / 2));
-          } else {
-#pragma unroll
-            for (int nn = 0; nn < 8; nn++) {  // the pair's first channel is in column block nn
-              const int c = 8 * nn - (CSA2_DI - rk);
-              if (c < 0 || c >= rk / 2) continue;
-              const float2* a = cs + c + 2 * (lane & 3);
-              // its second lies rk / 16 blocks on
-              float2& z = rk == 64 ? y[(nn + 4) & 7] : y[(nn + 2) & 7];
-              const float2 u = rotate_pair(y[nn].x, z.x, __ldg(a));
-              const float2 w = rotate_pair(y[nn].y, z.y, __ldg(a + 1));
-              y[nn] = make_float2(u.x, w.x);
-              z = make_float2(u.y, w.y);
-            }
-          }
-        }
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.idx_k + row * CSA2_DI) + (lane & 3);
-#pragma unroll
-        for (int nn = 0; nn < 8; nn++) dst[4 * nn] = pack_bf16x2(y[nn].x, y[nn].y);
-      }
-    }
+    if (ok) et_keys(p, g, buf, tmem, warp, lane);
     tc_fence_before();
-    alive = __syncthreads_and(ok);
-    tc_fence_after();
+    alive = bar_and<ET_GT>(1 + grp, ok);  // the rows are done with
+    if (more) fetch(tile + step);
+    if (more) et_check(p, g, tile + step, buf ^ 1, warp, lane);
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    bar_sync<ET_GT>(1 + grp);
   }
   if (!alive && t == 0) set_status(p.status, ST_TIMEOUT);
+  tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(s.tmem_base, 64);
+  if (threadIdx.x < 32) {
+    tc_fence_after();
+    tmem_dealloc(s.tmem_base, 64 * ET_GROUPS);
+  }
 }
 
 // The window entries of many tokens: one CTA per 16 of the last 128 tokens of a
@@ -479,12 +537,16 @@ cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st) {
                                     (int)ET_SMEM);
       });
       if (e != cudaSuccess) return e;
-      const int tiles = (p.total + ET_TOK - 1) / ET_TOK, sms = num_sms();
+      const int sms = num_sms();
+      ExtendParams q = p;
+      q.tile = 16;
+      while (q.tile < ET_TOK && (p.total + q.tile - 1) / q.tile > sms * ET_GROUPS) q.tile *= 2;
+      const int tiles = (p.total + q.tile - 1) / q.tile;
       cfg.gridDim = dim3(tiles < sms ? tiles : sms);
       cfg.blockDim = dim3(ET_NT);
       cfg.dynamicSmemBytes = ET_SMEM;
       trace_mark("extend", st);
-      if ((e = cudaLaunchKernelEx(&cfg, extend_tile_kernel, p)) != cudaSuccess) return e;
+      if ((e = cudaLaunchKernelEx(&cfg, extend_tile_kernel, q)) != cudaSuccess) return e;
       cfg.blockDim = dim3(EX_NT);
       cfg.dynamicSmemBytes = 0;
     }

@@ -201,6 +201,7 @@ struct ExtendParams {
   uint8_t* swa;           // [n_layers][batch][128][512] or NULL
   int32_t* swa_pos;
   int32_t* swa_len;
+  int32_t tile;           // tokens per tile of extend_tile_kernel: 16, 32 or 64
   uint32_t* status;
 };
 cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st);

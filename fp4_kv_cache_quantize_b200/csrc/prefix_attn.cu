@@ -98,10 +98,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-template <int N>
-__device__ __forceinline__ void bar_sync(int id) {
-  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
-}
 // Barrier of 128 threads that also tells whether any of them said so.
 __device__ __forceinline__ bool bar_or_128(int id, bool v) {
   uint32_t r;

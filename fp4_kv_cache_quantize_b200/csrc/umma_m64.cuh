@@ -32,6 +32,31 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Barrier of N threads of the CTA.
+template <int N>
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
+}
+// The same, and whether all of them said so.
+template <int N>
+__device__ __forceinline__ bool bar_and(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "n"(N)
+      : "memory");
+  return r != 0;
+}
+// Each thread of a warp reads 2 x 2 of eight columns, of 16 lanes: columns 2
+// (lane % 4) + {0, 1} of lane lane / 4, then of lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x1(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
 // Each thread of a warp reads 2 x 2 neighbours of every eight of 32 columns, of
 // 16 lanes.
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
