@@ -280,15 +280,21 @@ __device__ __forceinline__ void et_check(const ExtendParams& p, EtGroup& g, int 
   }
 }
 
-// The pieces in front of the rotated ones, packed.
+// The scale groups in front of the rotated channels, packed: 256 / tile threads
+// per row, one 16-channel group each in turn (a quarter-warp's 16-byte reads meet
+// different banks, a row's codes are written 32 bytes at a time or more).
 __device__ __forceinline__ void et_plain(const ExtendParams& p, const uint8_t* a, const EtGroup& g,
                                          int buf, int plain, int t) {
+  const int per_row = ET_GT / p.tile, r = t / per_row;
+  const int64_t row = g.row[buf][r];
+  if (row < 0) return;
 #pragma unroll 2
-  for (int i = t; i < p.tile * plain; i += ET_GT) {  // (whole warps: a multiple of 16 * 4)
-    const int r = i / plain, piece = i - r * plain;
-    float f[8];
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(a + et_at(r, piece)), f);
-    et_pack(p, f, g.row[buf][r], piece);
+  for (int q = t % per_row; q < plain / 2; q += per_row) {
+    uint8_t sb;
+    const uint2 codes = fp4_encode16(*reinterpret_cast<const uint4*>(a + et_at(r, 2 * q)),
+                                     *reinterpret_cast<const uint4*>(a + et_at(r, 2 * q + 1)), &sb);
+    reinterpret_cast<uint2*>(p.codes + row * (CSA2_D / 2))[q] = codes;
+    p.scales[row * (CSA2_D / 16) + q] = sb;
   }
 }
 

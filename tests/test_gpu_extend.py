@@ -228,6 +228,35 @@ def test_extend_many_sequences(lib, orc):
     c.check()
 
 
+@pytest.mark.parametrize("dims", [0, 32])
+def test_extend_packs_every_finite_bf16(lib, orc, dims):
+    """Both encoders (few and many tokens, rotated by position 0 or not) against
+    the oracle's on every finite bf16 value, next to group maxima that put the
+    scale anywhere, ties of every kind included."""
+    bits = torch.arange(1 << 16, dtype=torch.int32)
+    bits = bits[(bits & 0x7F80) != 0x7F80].to(torch.int16)  # finite
+    g = torch.Generator().manual_seed(1)
+    vals = bits[torch.randperm(len(bits), generator=g)][:65024 // 15 * 15].view(-1, 15)
+    big = torch.randint(0, 0x7F80, (len(vals), 1), generator=g).to(torch.int16)
+    x = torch.cat([vals, big], 1)
+    small = torch.randint(0x3C00, 0x4300, (len(vals), 16), generator=g).to(torch.int16)  # ties near 1
+    x = torch.cat([x, small]).view(-1)
+    x = x[:x.numel() // D * D].view(-1, D)
+    for part in (x, x[:300]):  # more than, and no more than, the few tokens' limit
+        T = len(part)
+        c = Case(lib, orc, [T], [0], L=0, dims=dims, idx_dims=0, pos="given")
+        c.x = part.view(torch.bfloat16)
+        c.d["x"].copy_(c.x)
+        c.pos.zero_()
+        c.d["pos"].zero_()
+        c.run()
+        lib.csa2_sync_status(c.ws)
+        codes, scales = orc.quantize_fp4(part.numpy().view(np.uint16))
+        row = rows_of(0, 0, T, c.stride, c.page_table)
+        assert torch.equal(c.d["codes"].cpu()[row], torch.from_numpy(codes))
+        assert torch.equal(c.d["scales"].cpu()[row], torch.from_numpy(scales))
+
+
 def test_extend_nothing(lib, orc):
     """No tokens at all: counters stay, nothing is written."""
     c = Case(lib, orc, [0, 0], [5, 6])
