@@ -174,8 +174,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle, without making a Stream object for it
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def status_string(status: int) -> str:

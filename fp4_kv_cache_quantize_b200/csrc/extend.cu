@@ -5,7 +5,7 @@
 // rotated and rounded once, and the last 128 tokens of the run go to every
 // layer's E4M3 window ring.  A sequence whose run does not fit is left alone as
 // a whole, so every CTA that writes for a sequence first checks the sequence's
-// whole run; extend_commit_kernel makes the same check and advances counters.
+// whole run; what advances the counters makes the same check.
 #include "csa2_internal.cuh"
 #include "umma_m64.cuh"
 #include "rope.cuh"
@@ -14,6 +14,7 @@ namespace csa2 {
 
 constexpr int EX_NT = 256;
 constexpr int EX_LAYERS_PER_CTA = EX_NT / 64;
+constexpr int EX_COMMIT_BATCH = 512;  // sequences whose counters the last CTA advances
 constexpr int EX_FEW = 512;  // tokens up to which each has a CTA of its own
 
 // Tokens [lo, hi) of sequence b; false if the offsets are out of order or do
@@ -60,7 +61,7 @@ __device__ __forceinline__ int64_t extend_row(const ExtendParams& p, int b, int6
 // threads together look at every page that it touches, and at the counters.
 __device__ __forceinline__ bool run_fits(const ExtendParams& p, int b, int count, int first,
                                          int step) {
-  if (p.swa && (__ldg(p.swa_pos + b) < 0 || __ldg(p.swa_pos + b) > 0x7FFFFFFF - count)) return false;
+  if (p.swa && (p.swa_pos[b] < 0 || p.swa_pos[b] > 0x7FFFFFFF - count)) return false;
   if (!p.x) return true;
   const int64_t n0 = p.n_rows[b], end = n0 + count;
   if (n0 < 0 || end > 0x7FFFFFFF) return false;
@@ -73,6 +74,59 @@ __device__ __forceinline__ bool run_fits(const ExtendParams& p, int b, int count
     ok = extend_row(p, b, last) >= 0;
   }
   return ok;
+}
+
+// Advances the counters of all sequences, once every write of the step has
+// landed: a thread per sequence whose run is short, a warp per one whose run is
+// not (`threads` threads, whole warps).
+__device__ __forceinline__ void extend_commit(const ExtendParams& p, int t, int threads) {
+  constexpr int SHORT = 128;  // at most three pages
+  auto advance = [&](int b, int count, bool ok) {
+    if (!ok) {
+      set_status(p.status, ST_DEVICE_CHECK);
+      return;
+    }
+    if (p.x) p.n_rows[b] += count;
+    if (p.swa) {
+      const int spos = p.swa_pos[b] + count;
+      p.swa_pos[b] = spos;
+      p.swa_len[b] = spos < CSA2_W ? spos : CSA2_W;
+    }
+  };
+  for (int b = t; b < p.batch; b += threads) {
+    int lo, hi;
+    const bool order = run_of(p, b, lo, hi);
+    if (!order) {
+      advance(b, 0, false);
+    } else if (hi - lo <= SHORT) {
+      advance(b, hi - lo, run_fits(p, b, hi - lo, 0, 1));
+    }
+  }
+  if (p.total <= SHORT) return;
+  for (int b = t >> 5; b < p.batch; b += threads >> 5) {
+    int lo, hi;
+    if (!run_of(p, b, lo, hi) || hi - lo <= SHORT) continue;
+    const bool ok = __all_sync(0xffffffffu, run_fits(p, b, hi - lo, t & 31, 32));
+    if ((t & 31) == 0) advance(b, hi - lo, ok);
+  }
+}
+
+// The last CTA of a launch to get here advances the counters: a launch less than
+// with a commit kernel.  Every CTA arrives after its last read of them; the
+// arrival counter (workspace header) is left at zero.
+__device__ __forceinline__ void extend_arrive(const ExtendParams& p) {
+  __shared__ int last;
+  if (!p.commit) return;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const uint32_t n = gridDim.x * gridDim.y;
+    last = atomicAdd(p.status + CSA2_WS_ARRIVE_WORD, 1u) == n - 1;
+    if (last) p.status[CSA2_WS_ARRIVE_WORD] = 0u;
+  }
+  __syncthreads();
+  if (!last) return;
+  extend_commit(p, threadIdx.x, blockDim.x);
 }
 
 // Eight channels of one window entry: rotated, E4M3, into its ring slot.
@@ -96,17 +150,15 @@ __device__ __forceinline__ void window_row(const ExtendParams& p, int b, int l, 
 // One CTA per token (few tokens): part 0 packs the entry and projects its key (256 threads:
 // 8 outputs x 16 channels each, partial sums reduced in a fixed order); parts
 // 1.. convert four layers' window entries each (64 threads per layer).
-__global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams p) {
+__device__ __forceinline__ void extend_token(const ExtendParams& p) {
   __shared__ float xs[CSA2_D];
   __shared__ float part[32][CSA2_DI + 1];
   __shared__ float ks[CSA2_DI];
   const int t = threadIdx.x, tok = blockIdx.x;
   const bool main_part = p.x != nullptr && blockIdx.y == 0;
-  pdl_launch_dependents();
-  pdl_wait();
 
   const int b = seq_of(p, tok);
-  if (b < 0) return;  // behind the last run (extend_commit_kernel records bad offsets)
+  if (b < 0) return;  // behind the last run (extend_commit records bad offsets)
   int lo, hi;
   const bool in_order = run_of(p, b, lo, hi);
   if (!__syncthreads_and(in_order && run_fits(p, b, hi - lo, t, EX_NT))) return;
@@ -173,7 +225,14 @@ __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams 
 
   const int l = (blockIdx.y - (p.x ? 1 : 0)) * EX_LAYERS_PER_CTA + (t >> 6);
   if (l >= p.n_layers || tok < hi - CSA2_W) return;
-  window_row(p, b, l, tok, __ldg(p.swa_pos + b) + (tok - lo), t & 63);
+  window_row(p, b, l, tok, p.swa_pos[b] + (tok - lo), t & 63);
+}
+
+__global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extend_token(p);
+  extend_arrive(p);
 }
 
 // ------------------------------------------------- many tokens: tiles of 64
@@ -475,52 +534,41 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
     tc_fence_after();
     tmem_dealloc(s.tmem_base, 64 * ET_GROUPS);
   }
+  extend_arrive(p);
 }
 
 // The window entries of many tokens: one CTA per 16 of the last 128 tokens of a
 // sequence's run and layer, 64 threads per row.
 constexpr int EW_TOK = 16;
-__global__ void __launch_bounds__(EX_NT) extend_window_kernel(const ExtendParams p) {
+__device__ __forceinline__ void extend_window(const ExtendParams& p) {
   const int t = threadIdx.x, b = blockIdx.x / (CSA2_W / EW_TOK), part = blockIdx.x % (CSA2_W / EW_TOK);
   const int l = blockIdx.y, ch = t & 63;
-  pdl_launch_dependents();
-  pdl_wait();
   int lo, hi;
   if (!run_of(p, b, lo, hi)) return;
   const int last = hi - part * EW_TOK, first = max(lo, last - EW_TOK);
   if (last <= lo) return;
   if (!__syncthreads_and(run_fits(p, b, hi - lo, t, EX_NT))) return;
-  const int spos0 = __ldg(p.swa_pos + b);
-  for (int tok = first + (t >> 6); tok < last; tok += EX_NT / 64) {
-    const int spos = spos0 + (tok - lo);
-    window_row(p, b, l, tok, spos, ch);
-  }
+  const int spos0 = p.swa_pos[b];
+  for (int tok = first + (t >> 6); tok < last; tok += EX_NT / 64)
+    window_row(p, b, l, tok, spos0 + (tok - lo), ch);
 }
 
-// Advances the counters once every write of the step has landed: one warp per
-// sequence.
+__global__ void __launch_bounds__(EX_NT) extend_window_kernel(const ExtendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extend_window(p);
+  extend_arrive(p);
+}
+
+// The same for large batches.
 __global__ void __launch_bounds__(EX_NT) extend_commit_kernel(const ExtendParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int b = (blockIdx.x * EX_NT + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (b >= p.batch) return;
-  int lo, hi;
-  bool ok = run_of(p, b, lo, hi);
-  ok = __all_sync(0xffffffffu, ok && run_fits(p, b, hi - lo, lane, 32));
-  if (lane != 0) return;
-  if (!ok) {
-    set_status(p.status, ST_DEVICE_CHECK);
-    return;
-  }
-  if (p.x) p.n_rows[b] += hi - lo;
-  if (p.swa) {
-    const int spos = p.swa_pos[b] + (hi - lo);
-    p.swa_pos[b] = spos;
-    p.swa_len[b] = spos < CSA2_W ? spos : CSA2_W;
-  }
+  extend_commit(p, blockIdx.x * EX_NT + threadIdx.x, gridDim.x * EX_NT);
 }
 
-cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st) {
+cudaError_t launch_extend(const ExtendParams& params, cudaStream_t st) {
+  ExtendParams p = params;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -529,40 +577,45 @@ cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  cudaError_t e;
+  // the last launch that writes also advances the counters, unless one CTA would
+  // be long at it
+  const bool in_last = p.batch <= EX_COMMIT_BATCH;
   if (p.total <= EX_FEW) {
+    p.commit = in_last;
     cfg.gridDim = dim3(p.total, (p.x ? 1 : 0) +
                                     (p.n_layers + EX_LAYERS_PER_CTA - 1) / EX_LAYERS_PER_CTA);
     trace_mark("extend", st);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, extend_token_kernel, p);
-    if (e != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, extend_token_kernel, p)) != cudaSuccess) return e;
   } else {
+    if (p.n_layers > 0) {
+      p.commit = in_last && !p.x;
+      cfg.gridDim = dim3(p.batch * (CSA2_W / EW_TOK), p.n_layers);
+      trace_mark("extend_window", st);
+      if ((e = cudaLaunchKernelEx(&cfg, extend_window_kernel, p)) != cudaSuccess) return e;
+    }
     if (p.x) {
       static PerDeviceOnce attr;
-      cudaError_t e = attr.run([](int&) {
+      e = attr.run([](int&) {
         return cudaFuncSetAttribute(extend_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)ET_SMEM);
       });
       if (e != cudaSuccess) return e;
       const int sms = num_sms();
-      ExtendParams q = p;
-      q.tile = 16;
-      while (q.tile < ET_TOK && (p.total + q.tile - 1) / q.tile > sms * ET_GROUPS) q.tile *= 2;
-      const int tiles = (p.total + q.tile - 1) / q.tile;
+      p.commit = in_last;
+      p.tile = 16;
+      while (p.tile < ET_TOK && (p.total + p.tile - 1) / p.tile > sms * ET_GROUPS) p.tile *= 2;
+      const int tiles = (p.total + p.tile - 1) / p.tile;
       cfg.gridDim = dim3(tiles < sms ? tiles : sms);
       cfg.blockDim = dim3(ET_NT);
       cfg.dynamicSmemBytes = ET_SMEM;
       trace_mark("extend", st);
-      if ((e = cudaLaunchKernelEx(&cfg, extend_tile_kernel, q)) != cudaSuccess) return e;
+      if ((e = cudaLaunchKernelEx(&cfg, extend_tile_kernel, p)) != cudaSuccess) return e;
       cfg.blockDim = dim3(EX_NT);
       cfg.dynamicSmemBytes = 0;
     }
-    if (p.n_layers > 0) {
-      cfg.gridDim = dim3(p.batch * (CSA2_W / EW_TOK), p.n_layers);
-      trace_mark("extend_window", st);
-      const cudaError_t e = cudaLaunchKernelEx(&cfg, extend_window_kernel, p);
-      if (e != cudaSuccess) return e;
-    }
   }
+  if (in_last) return cudaSuccess;
   cfg.gridDim = dim3((p.batch * 32 + EX_NT - 1) / EX_NT);
   trace_mark("extend_commit", st);
   return cudaLaunchKernelEx(&cfg, extend_commit_kernel, p);

@@ -62,6 +62,9 @@ constexpr int SC_TILE = 128;
 // Word of the workspace header where the scan's tile counter lives (the
 // status word is word 0); it is zero between launches.
 constexpr int CSA2_WS_SCHED_WORD = 16;
+// Word of the header in which the cache extension's CTAs count their arrival;
+// zero between launches.
+constexpr int CSA2_WS_ARRIVE_WORD = 17;
 constexpr int CSA2_SCAN_QUERIES = 8;  // queries one scan launch scores (MMA N <= 64)
 
 constexpr int RS_MAX_JOBS = 8;
@@ -202,6 +205,7 @@ struct ExtendParams {
   int32_t* swa_pos;
   int32_t* swa_len;
   int32_t tile;           // tokens per tile of extend_tile_kernel: 16, 32 or 64
+  int32_t commit;         // this launch's last CTA advances the counters
   uint32_t* status;
 };
 cudaError_t launch_extend(const ExtendParams& p, cudaStream_t st);

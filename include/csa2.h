@@ -103,9 +103,10 @@ const char *csa2_status_string(csa2_status s);
 /* Thread-local text of the last error returned on this thread ("" if none). */
 const char *csa2_last_error(void);
 
-/* Bytes at the start of every workspace: the device status word (word 0)
- * and the Full scan's tile counter (word 16), which every scan launch
- * returns to zero before it completes.  A workspace serves one call at a
+/* Bytes at the start of every workspace: the device status word (word 0),
+ * the Full scan's tile counter (word 16) and the cache extension's arrival
+ * counter (word 17), which every launch that uses one returns to zero before
+ * it completes.  A workspace serves one call at a
  * time (calls enqueued on one stream, or otherwise ordered). */
 #define CSA2_WS_HEADER 256
 /* Zero the header of a workspace (status word and scan counter; enqueued on
@@ -440,7 +441,8 @@ csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32
  * unmapped page, a negative counter, token offsets out of order or beyond
  * total) is left unchanged as a whole, rows, windows and counters, and
  * CSA2_ERR_DEVICE_CHECK is recorded.  ws: at least CSA2_WS_HEADER bytes.
- * Two or three launches; asynchronous on stream.
+ * ws must have been initialised once (csa2_workspace_init).  One to three
+ * launches; asynchronous on stream.
  */
 typedef struct {
   csa2_kv_view kv;
