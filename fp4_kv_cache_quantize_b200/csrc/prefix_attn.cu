@@ -23,26 +23,44 @@
 
 namespace csa2 {
 
-// Roles of a CTA: eight warps turn key tiles into fp16, eight run the softmax,
-// one thread issues the MMAs.  Key tiles are 64 keys so that two fit next to the
+// Roles of a CTA: eight warps turn key tiles into fp16, sixteen run the softmax,
+// one thread issues the S^T products and one the O^T products, one warp works out
+// which tiles come next.  Key tiles are 64 keys so that two fit next to the
 // queries: while one is multiplied, the next is written.  S^T then is an M = 64
 // product at half the tensor core's rate, but one that shared memory could not
 // feed faster anyway (4 KB of operands in 32 cycles); a single 128-key tile,
 // filled, multiplied and filled again, took twice as long.
-constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 8;
+constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 16;
 constexpr int PA_MMA_WARP = PA_DQ_WARPS + PA_SM_WARPS;
-constexpr int PA_RUN_NT = 32 * (PA_MMA_WARP + 1);  // threads with a role
-constexpr int PA_NT = 32 * (PA_MMA_WARP + 4);      // whole warpgroups: registers move between them
-// Registers per thread: launched with 96 (640 threads), then 256 x 88 + 256 x 112
-// + 128 x 80 = 61,440, the launch's.  With 96 for all, the loops' spills missed
-// the little L1 that the shared memory leaves and cost most of their time.
-constexpr int PA_DQ_REGS = 88, PA_SM_REGS = 112, PA_MMA_REGS = 80;
+constexpr int PA_NT = 32 * (PA_MMA_WARP + 3);
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
 constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
 constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
 constexpr uint32_t PA_TMEM_COLS = 512;
 constexpr float PA_SHIFT = 7.0f, PA_SLACK = 8.0f;
 constexpr float PA_NONE = -1e30f;  // reference of a row that has met no key
+
+// mbar_wait that sleeps until the phase completes, in naps of up to 20 us: the
+// waits' polling otherwise takes issue slots from the warps that work.
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  auto nap = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (nap()) return true;
+  const long long t0 = clock64();
+  while (!nap()) {
+    if (*abort || clock64() - t0 > kWaitCycles) return false;
+  }
+  return true;
+}
 
 // One contiguous run of key tiles of one segment.
 struct PaRun {
@@ -51,6 +69,7 @@ struct PaRun {
   int kt, kt_end;    // key tiles (none if kt_end <= kt)
   int line;          // how far the run goes on the line
   int own_tiles;     // tiles at or past this are window tiles (own segments)
+  int kt_cache;      // cache tiles of the run end here
   int first_pos;     // position of key 0 of tile 0
   int n_keys;        // positions of the row map end here
   int win_lo, n_win; // first window row of tile own_tiles, rows of the window
@@ -69,7 +88,7 @@ struct PaSmem {
   alignas(16) float fac[PA_ROWS];             // what a raised reference scales O by
   alignas(16) int lo[2][PA_ROWS], hi[2][PA_ROWS];  // cache, window: visible keys [lo, hi)
   int lo_max[2], hi_min[2];                   // keys [lo_max, hi_min) are visible to all rows
-  // per tile: whether a key is missing (1) or holds a NaN (2), by quarter
+  // per tile: whether a key is missing (1) or holds a NaN (2), by reading thread
   alignas(16) uint8_t key[2][PA_KEYS][4];
   float red[4][PA_ROWS];
   int cum[CSA2_PREFIX_MAX_BATCH + 1];         // own tiles on the line of sequences < b
@@ -110,28 +129,6 @@ __device__ __forceinline__ bool bar_or_128(int id, bool v) {
   return r != 0;
 }
 
-// Pool row of key r of tile kt, or -1: none (a mapping outside the pool is
-// recorded).
-__device__ __forceinline__ int64_t pa_row(const PrefixParams& p, const PaRun& run, int kt, int r) {
-  const int pos = run.first_pos + kt * PA_KEYS + r;
-  if (kt >= run.kt_end || (run.own && kt >= run.own_tiles) || pos >= run.n_keys) return -1;
-  int64_t row;
-  if (p.page_table) {
-    const int page = pos >> 6;
-    const int64_t pid =
-        page < p.max_pages ? (int64_t)__ldg(p.page_table + (int64_t)run.seq * p.max_pages + page)
-                           : -1;
-    row = pid < 0 ? -1 : pid * 64 + (pos & 63);
-  } else {
-    row = (int64_t)run.seq * p.seq_stride + pos;
-  }
-  if (row < 0 || row >= p.pool_rows) {
-    set_status(p.status, ST_DEVICE_CHECK);
-    return -1;
-  }
-  return row;
-}
-
 // Loads that stay where they are written: a plain read-only load may be moved
 // down to its use, one tile later, which put a whole memory latency in front of
 // every block.
@@ -146,6 +143,36 @@ __device__ __forceinline__ uint32_t ld_now_u16(const void* a) {
   uint16_t v;
   asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(a));
   return v;
+}
+
+__device__ __forceinline__ int ld_now_s32(const void* a) {
+  int v;
+  asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
+
+// The row map in two steps, so that the page id's latency has a tile's time:
+// the page id of a position (not waited for), then its pool row.  -1: none (a
+// mapping outside the pool is recorded).
+__device__ __forceinline__ int pa_page(const PrefixParams& p, const PaRun& run, int kt, int r) {
+  const int pos = run.first_pos + kt * PA_KEYS + r;
+  if (kt >= run.kt_cache || pos >= run.n_keys) return -1;
+  if (!p.page_table) return 0;
+  const int page = pos >> 6;
+  if (page >= p.max_pages) return -2;
+  return ld_now_s32(p.page_table + (int64_t)run.seq * p.max_pages + page);
+}
+__device__ __forceinline__ int64_t pa_row(const PrefixParams& p, const PaRun& run, int kt, int r,
+                                          int pid) {
+  const int pos = run.first_pos + kt * PA_KEYS + r;
+  if (kt >= run.kt_cache || pos >= run.n_keys) return -1;
+  const int64_t row = p.page_table ? (int64_t)pid * 64 + (pos & 63)
+                                   : (int64_t)run.seq * p.seq_stride + pos;
+  if (pid < 0 || row >= p.pool_rows) {
+    set_status(p.status, ST_DEVICE_CHECK);
+    return -1;
+  }
+  return row;
 }
 
 // Whether a byte of w is an E4M3 NaN (0x7F or 0xFF).
@@ -204,6 +231,25 @@ __device__ __forceinline__ uint4 pa_e4m3x8(uint32_t a, uint32_t b) {
     h[k] = pa_h2u(__hmul2(e4m3x2_as_f16(w), two));
   }
   return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// umma_bf16 with the descriptors as two words: only the low one (the start
+// address) changes from product to product, so a step costs one 32-bit addition
+// per operand.
+struct PaDesc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit PaDesc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+};
+__device__ __forceinline__ void pa_umma(uint32_t d_tmem, PaDesc a, uint32_t a_off, PaDesc b,
+                                        uint32_t b_off, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a.lo + a_off), "r"(a.hi), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc),
+      "r"((uint32_t)accumulate)
+      : "memory");
 }
 
 // S^T (M = 64 keys) and O^T (M = 128 channels) products; n: query rows of the
@@ -269,6 +315,7 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
   run.kt_end = run.kt + (int)(min(seg_end, tile_end) - tile);
   run.line = run.kt_end - run.kt;
   run.kt = max(run.kt, 0);
+  run.kt_cache = min(run.kt_end, run.own_tiles);
   return run;
 }
 
@@ -276,12 +323,12 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
 __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& run, PaSmem& s,
                                            int warp, int lane) {
       // Q' = Q * 2^e in fp16, max |Q'| of a row in [2^14, 2^15): one warp per row,
-  // 16 channels per lane, four rows' loads in flight
+  // 16 channels per lane, two rows' loads in flight
 #pragma unroll 1
-  for (int h0 = warp; h0 < run.n_rows; h0 += 4 * PA_SM_WARPS) {
-    uint4 v[4][2];
+  for (int h0 = warp; h0 < run.n_rows; h0 += 2 * PA_SM_WARPS) {
+    uint4 v[2][2];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
+    for (int u = 0; u < 2; u++) {
       const int h = min(h0 + u * PA_SM_WARPS, run.n_rows - 1);
       const uint4* src =
           reinterpret_cast<const uint4*>(p.q + (int64_t)(run.row0 + h) * CSA2_D) + 2 * lane;
@@ -289,7 +336,7 @@ __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& r
       v[u][1] = __ldg(src + 1);
     }
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
+    for (int u = 0; u < 2; u++) {
       const int h = h0 + u * PA_SM_WARPS;
       if (h >= run.n_rows) break;
       uint32_t mx = 0u;
@@ -420,31 +467,33 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   // Per run of tiles: BAR_RUN (the run is known), BAR_Q (its queries are in
   // shared memory; softmax and MMA warps), the tiles, BAR_RUN (all is done).
   // Tile i of the CTA uses buffers i & 1; their barriers' phase is (i >> 1) & 1.
-  constexpr int BAR_RUN = 3, BAR_Q = 4;
-  constexpr int Q_THREADS = 32 * (PA_SM_WARPS + 1);
+  // (1 to 4: the softmax warps of 16 rows, 5: all softmax warps)
+  constexpr int BAR_RUN = 6, BAR_Q = 7;
+  constexpr int Q_THREADS = 32 * (PA_SM_WARPS + 2);
   uint32_t i = 0;
   if (warp < PA_DQ_WARPS) {
     // ------------------------------------------------ key tiles to fp16
     // Lane (seg, r8) of a warp has key r8 of the warp's eight and 32 channels (16
     // code bytes) of each 128-channel block: a load of the warp touches 8 rows by
-    // 64 consecutive bytes, and a quarter-warp's 16-byte stores go to 8 rows,
-    // whose swizzle gives them different banks.  The next tile's codes are on
-    // their way while this one's wait for a free buffer and are turned.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_DQ_REGS));
+    // 64 consecutive bytes, and a quarter-warp's 16-byte stores go to 8 rows, whose
+    // swizzle gives them different banks.  The next tile's codes are on their way
+    // while this one's wait for a free buffer and are turned.
     const int seg = lane >> 3, r = 8 * warp + (lane & 7), sw = lane & 7, cc = 4 * (seg & 1);
     for (;;) {
-      bar_sync<PA_RUN_NT>(BAR_RUN);
-      const PaRun run = s.run;
+      bar_sync<PA_NT>(BAR_RUN);
+      const PaRun& run = s.run;
       if (!run.valid) break;
+      const int kt_end = run.kt_end, kt_cache = run.kt_cache;
       uint4 v[4], nv[4];       // by block: this tile's codes, the next one's
       uint32_t sc[4], nsc[4];  // the two scales of the same 32 channels
       auto load = [&](int64_t row) {
+        if (row < 0) return;
+        const uint8_t* c = p.codes + row * (CSA2_D / 2) + 16 * seg;
+        const uint8_t* f = p.scales + row * (CSA2_D / 16) + 2 * seg;
 #pragma unroll
         for (int b = 0; b < 4; b++) {
-          if (row >= 0) {
-            nv[b] = ld_now_v4(p.codes + row * (CSA2_D / 2) + 64 * b + 16 * seg);
-            nsc[b] = ld_now_u16(p.scales + row * (CSA2_D / 16) + 8 * b + 2 * seg);
-          }
+          nv[b] = ld_now_v4(c + 64 * b);
+          nsc[b] = ld_now_u16(f + 8 * b);
         }
       };
 #pragma unroll
@@ -452,27 +501,28 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         nv[b] = make_uint4(0u, 0u, 0u, 0u);
         nsc[b] = 0u;
       }
-      int64_t row, next = pa_row(p, run, run.kt, r), after = pa_row(p, run, run.kt + 1, r);
+      int pid = pa_page(p, run, run.kt, r), pid1 = pa_page(p, run, run.kt + 1, r);
+      int64_t row, next = pa_row(p, run, run.kt, r, pid);
       load(next);
-      const int kt_cache = run.own ? min(run.own_tiles, run.kt_end) : run.kt_end;
       int kt = run.kt;
 #pragma unroll 1
       for (; kt < kt_cache; kt++, i++) {
+        pid = pid1;
+        pid1 = pa_page(p, run, kt + 2, r);
         row = next;
-        next = after;
 #pragma unroll
         for (int b = 0; b < 4; b++) {
           v[b] = nv[b];
           sc[b] = nsc[b];
         }
+        next = pa_row(p, run, kt + 1, r, pid);
         load(next);
-        after = pa_row(p, run, kt + 2, r);
         // A key that is not there, or whose values hold a NaN, becomes zeros: the
         // P = 0 of a row that must not see it would turn NaN in the product
         const bool nan = has_nan(sc[0] | (sc[1] << 16)) || has_nan(sc[2] | (sc[3] << 16));
         const bool zero = row < 0 || nan;
         uint8_t* dst = s.tile[i & 1] + (seg >> 1) * PA_KB + r * 128;
-        if (i >= 2) mbar_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
+        if (i >= 2) pa_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
         s.key[i & 1][r][seg] = (uint8_t)(row < 0 ? 1 : (nan ? 2 : 0));
 #pragma unroll
         for (int b = 0; b < 4; b++) {
@@ -490,7 +540,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         if (lane == 0) mbar_arrive(&s.full[i & 1]);
       }
 #pragma unroll 1
-      for (; kt < run.kt_end; kt++, i++) {  // window tiles
+      for (; kt < kt_end; kt++, i++) {  // window tiles
         const int w = run.win_lo + (kt - run.own_tiles) * PA_KEYS + r;
         uint4 a[8];
         bool nan = false;
@@ -506,7 +556,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             nan |= has_nan(a[b].x) || has_nan(a[b].y) || has_nan(a[b].z) || has_nan(a[b].w);
         }
         uint8_t* dst = s.tile[i & 1] + (seg >> 1) * PA_KB + r * 128;
-        if (i >= 2) mbar_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
+        if (i >= 2) pa_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
         s.key[i & 1][r][seg] = (uint8_t)(w >= run.n_win ? 1 : (nan ? 2 : 0));
 #pragma unroll
         for (int b = 0; b < 8; b++) {
@@ -520,38 +570,27 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[i & 1]);
       }
-      bar_sync<PA_RUN_NT>(BAR_RUN);
+      bar_sync<PA_NT>(BAR_RUN);
     }
   } else if (warp < PA_MMA_WARP) {
     // --------------------------------------------------------- softmax
-    // Warp (quad, half): keys 16 quad + [0, 16), query rows 32 half + [0, 32).  An
+    // Warp (quad, part): keys 16 quad + [0, 16), query rows 16 part + [0, 16).  An
     // M = 64 accumulator has its rows in lanes 0..15 of each TMEM quarter; read as
     // 16 x 256 bits, a thread holds keys lane / 4 and lane / 4 + 8 by columns
-    // 8 n + 2 (lane % 4) + {0, 1}.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_SM_REGS));
-    const int w = warp - PA_DQ_WARPS, quad = w & 3, half = w >> 2;
+    // 8 n + 2 (lane % 4) + {0, 1}, n < 2.
+    const int w = warp - PA_DQ_WARPS, quad = w & 3, part = w >> 2;
     const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-    const int c0 = 32 * half + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
-    int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
-    const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
+    const int c0 = 16 * part + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
+    const PaRun& run = s.run;
     for (;;) {
-      if (w == 0) {
-        PaRun r;
-        do {  // skips what holds empty tiles only
-          r = pa_next_run(p, pl, s.cum, tile, tile_end, s.abort != 0);
-          if (r.valid) tile += r.line;
-        } while (r.valid && r.kt_end <= r.kt);
-        if (lane == 0) s.run = r;
-      }
-      bar_sync<PA_RUN_NT>(BAR_RUN);
-      const PaRun run = s.run;
+      bar_sync<PA_NT>(BAR_RUN);
       if (!run.valid) break;
       pa_queries(p, run, s, w, lane);
       bar_sync<Q_THREADS>(BAR_Q);
-      const bool active = 32 * half < run.n_rows;  // per warp
-      float scl[8], m[8], l[8];
+      const bool active = 16 * part < run.n_rows;  // per warp
+      float scl[4], m[4], l[4];
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
+      for (int j = 0; j < 4; j++) {
         const int c = c0 + 8 * (j >> 1) + (j & 1);
         scl[j] = c < run.n_rows ? s.scl[c] : 0.0f;
         m[j] = PA_NONE;
@@ -562,49 +601,56 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         const bool win = run.own && kt >= run.own_tiles;
         const int first = win ? run.win_lo + (kt - run.own_tiles) * PA_KEYS
                               : run.first_pos + kt * PA_KEYS;
-        if (!mbar_wait(&s.s_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
-        mbar_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort);  // (complete) the keys' flags
+        if (!pa_wait(&s.s_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
+        pa_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort);  // (complete) the keys' flags
         __syncwarp();
         tc_fence_after();
         if (active) {
-          uint32_t acc[16];
-          tmem_ld_16x256b_x4(tmem + lane_base + PA_S_COL + PA_ROWS * (i & 1) + 32 * half, acc);
           const uint32_t f0 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0]);
           const uint32_t f1 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0 + 8]);
           const bool plain = first >= s.lo_max[win] && first + PA_KEYS <= s.hi_min[win] &&
                              __all_sync(0xffffffffu, (f0 | f1) == 0);
-          tmem_ld_wait();
-          // x[4 n + 2 k + e]: key k0 + 8 k, row c0 + 8 n + e
-          float x[16];
-#pragma unroll
-          for (int j = 0; j < 16; j++)
-            x[j] = __uint_as_float(acc[j]) * scl[2 * (j >> 2) + (j & 1)];
-          if (!plain) {
-#pragma unroll
-            for (int j = 0; j < 16; j++) {
-              const int c = c0 + 8 * (j >> 2) + (j & 1), key = first + k0 + 8 * ((j >> 1) & 1);
-              const uint32_t f = (j >> 1) & 1 ? f1 : f0;
-              const bool see = !(f & 1u) && key >= s.lo[win][c] && key < s.hi[win][c];
-              x[j] = see ? (f ? __int_as_float(0x7FC00000) : x[j]) : -INFINITY;
-            }
-          }
-          float over = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 16; j++) over = fmaxf(over, x[j] - m[2 * (j >> 2) + (j & 1)]);
-          if (bar_or_128(1 + half, over > PA_SHIFT + PA_SLACK)) {
-            // some logit is far above its reference: raise the references to the
-            // rows' maxima and scale what was summed
+          // x[4 n + 2 k + e]: key k0 + 8 k, row c0 + 8 n + e: the logit less f times
+          // the row's reference
+          auto logits = [&](float f, float(&x)[8]) {
+            uint32_t acc[8];
+            tmem_ld_16x256b_x2(tmem + lane_base + PA_S_COL + PA_ROWS * (i & 1) + 16 * part, acc);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 8; j++) {
+              const int c = 2 * (j >> 2) + (j & 1);
+              x[j] = fmaf(__uint_as_float(acc[j]), scl[c], f * m[c]);
+            }
+            if (!plain) {
+#pragma unroll
+              for (int j = 0; j < 8; j++) {
+                const int c = c0 + 8 * (j >> 2) + (j & 1), key = first + k0 + 8 * ((j >> 1) & 1);
+                const uint32_t bad = (j >> 1) & 1 ? f1 : f0;
+                const bool see = !(bad & 1u) && key >= s.lo[win][c] && key < s.hi[win][c];
+                x[j] = see ? (bad ? __int_as_float(0x7FC00000) : x[j]) : -INFINITY;
+              }
+            }
+          };
+          float x[8];
+          logits(-1.0f, x);
+          float over = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) over = fmaxf(over, fmaxf(x[j], x[j + 1]));
+          if (bar_or_128(1 + part, over > PA_SHIFT + PA_SLACK)) {
+            // some logit is far above its reference: raise the references to the
+            // rows' maxima and scale what was summed
+            logits(0.0f, x);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
               float mx = fmaxf(x[4 * (j >> 1) + (j & 1)], x[4 * (j >> 1) + 2 + (j & 1)]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               if (lane < 4) s.red[quad][c0 + 8 * (j >> 1) + (j & 1)] = mx;
             }
-            bar_or_128(1 + half, false);
+            bar_or_128(1 + part, false);
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
+            for (int j = 0; j < 4; j++) {
               const int c = c0 + 8 * (j >> 1) + (j & 1);
               const float mx = fmaxf(fmaxf(s.red[0][c], s.red[1][c]), fmaxf(s.red[2][c], s.red[3][c]));
               const float top = fmaxf(m[j], mx - PA_SHIFT), f = ex2(m[j] - top);
@@ -612,35 +658,35 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
               l[j] *= f;
               if (quad == 0 && lane < 4) s.fac[c] = f;
             }
-            bar_or_128(1 + half, false);
+            bar_or_128(1 + part, false);
             if (kt != run.kt) {
               // the products up to the last tile's are in O
-              if (!mbar_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
+              if (!pa_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
-              for (int g = 0; g < 8; g++) {  // channel block g / 2, 16 of the 32 rows
-                const int c = 32 * half + 16 * (g & 1);
-                const uint32_t at = tmem + lane_base + 64 * (g >> 1) + c;
+              for (int cb = 0; cb < 4; cb++) {  // channel blocks
+                const uint32_t at = tmem + lane_base + 64 * cb + 16 * part;
                 uint32_t o[16];
                 tmem_ld_x16(at, o);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; j++)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * s.fac[c + j]);
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * s.fac[16 * part + j]);
                 tmem_st_x16(at, o);
               }
               tmem_st_wait();
             }
+            logits(-1.0f, x);
           }
           uint8_t* dst = s.p[i & 1] + k0 * 128 + 4 * (lane & 3);
 #pragma unroll
-          for (int n = 0; n < 4; n++) {
-            const float p0 = ex2(x[4 * n] - m[2 * n]), p1 = ex2(x[4 * n + 1] - m[2 * n + 1]);
-            const float p2 = ex2(x[4 * n + 2] - m[2 * n]), p3 = ex2(x[4 * n + 3] - m[2 * n + 1]);
+          for (int n = 0; n < 2; n++) {
+            const float p0 = ex2(x[4 * n]), p1 = ex2(x[4 * n + 1]);
+            const float p2 = ex2(x[4 * n + 2]), p3 = ex2(x[4 * n + 3]);
             l[2 * n] += p0 + p2;
             l[2 * n + 1] += p1 + p3;
-            const uint32_t at = (uint32_t)((4 * half + n) ^ (k0 & 7)) << 4;  // (k0 + 8 alike)
+            const uint32_t at = (uint32_t)((2 * part + n) ^ (k0 & 7)) << 4;  // (k0 + 8 alike)
             *reinterpret_cast<uint32_t*>(dst + at) = pa_h2u(__floats2half2_rn(p0, p1));
             *reinterpret_cast<uint32_t*>(dst + 1024 + at) = pa_h2u(__floats2half2_rn(p2, p3));
           }
@@ -652,12 +698,12 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       }
       // ---- the run's partial: O [row][channel], (max, sum) per row.  The last
       // tile's commit covers every product.
-      if (!mbar_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
+      if (!pa_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
       __syncwarp();
       tc_fence_after();
       if (active) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
+        for (int j = 0; j < 4; j++) {
           float v = l[j];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -667,92 +713,94 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             if (quad == 0) s.fac[c] = m[j];
           }
         }
-        bar_or_128(1 + half, false);
-        const int c = 32 * half + lane;
-        if (quad == 0 && c < run.n_rows) {
+        bar_or_128(1 + part, false);
+        const int c = 16 * part + lane;
+        if (quad == 0 && lane < 16) {
           p.part_ml[2 * (run.slot + c)] = s.fac[c];
           p.part_ml[2 * (run.slot + c) + 1] =
               (s.red[0][c] + s.red[1][c]) + (s.red[2][c] + s.red[3][c]);
         }
 #pragma unroll 2
-        for (int g = 0; g < 8; g++) {  // channel block g / 2, 16 of the 32 rows
-          const int r0 = 32 * half + 16 * (g & 1);
-          if (r0 >= run.n_rows) continue;
+        for (int cb = 0; cb < 4; cb++) {
           uint32_t o[16];
-          tmem_ld_x16(tmem + lane_base + 64 * (g >> 1) + r0, o);
+          tmem_ld_x16(tmem + lane_base + 64 * cb + 16 * part, o);
           tmem_ld_wait();
-          float* dst = p.part_o + (run.slot + r0) * CSA2_D + 128 * (g >> 1) +
+          float* dst = p.part_o + (run.slot + 16 * part) * CSA2_D + 128 * cb +
                        pa_channel(32 * quad + lane);
 #pragma unroll
           for (int j = 0; j < 16; j++) dst[j * CSA2_D] = __uint_as_float(o[j]) * PA_TILE_SCALE;
         }
         tc_fence_before();
       }
-      bar_sync<PA_RUN_NT>(BAR_RUN);
+      bar_sync<PA_NT>(BAR_RUN);
     }
   } else {
     // ------------------------------------------------------ the products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_MMA_REGS));
-    const uint64_t qd = sdesc_k128(smem_u32(s.q));
-    const uint64_t pd = sdesc_mn128(smem_u32(s.p[0]), PA_KEYS * 128, 1024);
-    const uint64_t kd = sdesc_k128(smem_u32(s.tile[0]));
-    const uint64_t vd = sdesc_mn128(smem_u32(s.tile[0]), PA_KB, 1024);
-    while (warp == PA_MMA_WARP) {  // (the warpgroup's other warps have no work)
-      bar_sync<PA_RUN_NT>(BAR_RUN);
-      const int n_tiles = s.run.kt_end - s.run.kt, n_rows = s.run.n_rows;
+    // S^T from one warp, O^T from another: each waits for its own input only (one
+    // thread that took them in turn would hold up the other's), and the loops stay
+    // small.  A tile's buffers are free again once its O^T step is done, which
+    // follows its S^T and its softmax.
+    if (warp == PA_MMA_WARP + 2) {
+      int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
+      const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
+      for (bool valid = true; valid;) {
+        PaRun r;
+        do {  // skips what holds empty tiles only
+          r = pa_next_run(p, pl, s.cum, tile, tile_end, s.abort != 0);
+          if (r.valid) tile += r.line;
+        } while (r.valid && r.kt_end <= r.kt);
+        if (lane == 0) s.run = r;
+        valid = r.valid;
+        bar_sync<PA_NT>(BAR_RUN);
+        if (valid) bar_sync<PA_NT>(BAR_RUN);
+      }
+    }
+    while (warp <= PA_MMA_WARP + 1) {
+      bar_sync<PA_NT>(BAR_RUN);
       if (!s.run.valid) break;
+      const uint32_t begin = i, end = i + (uint32_t)(s.run.kt_end - s.run.kt);
+      const uint32_t id = pa_idesc(s.run.n_rows, warp != PA_MMA_WARP);
       bar_sync<Q_THREADS>(BAR_Q);
       tc_fence_after();
-      const uint32_t id_s = pa_idesc(n_rows, false), id_o = pa_idesc(n_rows, true);
       const bool leader = elect_one();
-      // The next S^T waits for its tile, the next O^T step for its P; whichever is
-      // ready goes, the O^T step first (it frees a tile buffer).  In a fixed order
-      // one of them would hold up the other's input: with S^T first, filling a
-      // tile and multiplying took turns (5.1K instead of 3.0K cycles a tile).
-      const uint32_t end = i + n_tiles;
-      uint32_t js = i;  // next S^T; i: next O^T
-      const uint32_t begin = i;
-      long long t0 = clock64();
+      if (warp == PA_MMA_WARP) {
+        const PaDesc qd(sdesc_k128(smem_u32(s.q))), kd(sdesc_k128(smem_u32(s.tile[0])));
 #pragma unroll 1
-      while (i < end) {
-        if (i < js && mbar_test_warp(&s.p_full[i & 1], (i >> 1) & 1)) {
+        for (; i < end; i++) {
+          if (!pa_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
           __syncwarp();
           tc_fence_after();
-          // O^T += V^T P^T: four channel blocks, K = 64 keys in four steps
-          if (leader) {
-            const uint64_t a = vd + ((i & 1) * ((8 * PA_KB) >> 4));
-            const uint64_t b = pd + ((i & 1) * ((PA_KEYS * 128) >> 4));
-#pragma unroll
-            for (uint32_t j = 0; j < 16; j++)
-              umma_bf16(tmem + 64 * (j & 3), a + (((j & 3) * 2 * PA_KB + (j >> 2) * 2048) >> 4),
-                        b + (((j >> 2) * 2048) >> 4), id_o, i != begin || j >= 4);
-            umma_commit(&s.empty[i & 1]);
-          }
-          i++;
-          t0 = clock64();
-        } else if (js < end && js < i + 2 && mbar_test_warp(&s.full[js & 1], (js >> 1) & 1)) {
-          __syncwarp();
-          tc_fence_after();
-          // S^T = K Q'^T: K = 512 in 32 steps
-          if (leader) {
-            const uint64_t a = kd + ((js & 1) * ((8 * PA_KB) >> 4));
-            const uint32_t d = tmem + PA_S_COL + PA_ROWS * (js & 1);
+          if (leader) {  // S^T = K Q'^T: K = 512, eight chunks of four steps
+            const uint32_t a = (i & 1) * ((8 * PA_KB) >> 4);
+            const uint32_t d = tmem + PA_S_COL + PA_ROWS * (i & 1);
 #pragma unroll
             for (uint32_t k = 0; k < 32; k++)
-              umma_bf16(d, a + (((k >> 2) * PA_KB + 32 * (k & 3)) >> 4),
-                        qd + (((k >> 2) * PA_QKB + 32 * (k & 3)) >> 4), id_s, k != 0);
-            umma_commit(&s.s_full[js & 1]);
+              pa_umma(d, kd, a + (((k >> 2) * PA_KB) >> 4) + 2 * (k & 3), qd,
+                      (((k >> 2) * PA_QKB) >> 4) + 2 * (k & 3), id, k != 0);
+            umma_commit(&s.s_full[i & 1]);
           }
-          js++;
-          t0 = clock64();
-        } else if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles || *(volatile int*)&s.abort)) {
-          s.abort = 1;  // nothing came: the other roles stop too
-          break;
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        const PaDesc pd(sdesc_mn128(smem_u32(s.p[0]), PA_KEYS * 128, 1024));
+        const PaDesc vd(sdesc_mn128(smem_u32(s.tile[0]), PA_KB, 1024));
+#pragma unroll 1
+        for (; i < end; i++) {
+          if (!pa_wait(&s.p_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
+          __syncwarp();
+          tc_fence_after();
+          if (leader) {  // O^T += V^T P^T: K = 64 keys in four steps, four channel blocks
+            const uint32_t a = (i & 1) * ((8 * PA_KB) >> 4), b = (i & 1) * ((PA_KEYS * 128) >> 4);
+#pragma unroll
+            for (uint32_t k = 0; k < 16; k++)
+              pa_umma(tmem + 64 * (k & 3), vd, a + (((k & 3) * 2 * PA_KB + (k >> 2) * 2048) >> 4), pd,
+                      b + (((k >> 2) * 2048) >> 4), id, i != begin || k >= 4);
+            umma_commit(&s.empty[i & 1]);
+          }
+          __syncwarp();
+        }
       }
-      i = end;
-      bar_sync<PA_RUN_NT>(BAR_RUN);
+      bar_sync<PA_NT>(BAR_RUN);
     }
   }
   if (s.abort && t == 0) set_status(p.status, ST_TIMEOUT);
