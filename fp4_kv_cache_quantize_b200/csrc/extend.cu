@@ -265,7 +265,7 @@ struct EtSmem {
   EtGroup g[ET_GROUPS];
   uint32_t tmem_base;
 };
-constexpr size_t ET_SMEM = sizeof(EtSmem) + 1024;
+constexpr size_t ET_SMEM = sizeof(EtSmem);
 
 __device__ __forceinline__ uint32_t et_at(int row, int piece) {
   return (uint32_t)((piece >> 3) * ET_KB + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
@@ -452,9 +452,8 @@ __device__ __forceinline__ void et_keys(const ExtendParams& p, const EtGroup& g,
 }
 
 __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  EtSmem& s = *reinterpret_cast<EtSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                         ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // (not rounded up: a generic pointer then)
+  EtSmem& s = *reinterpret_cast<EtSmem*>(smem_raw);
   const int grp = __shfl_sync(0xffffffffu, threadIdx.x / ET_GT, 0);
   const int t = threadIdx.x % ET_GT, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
   const int n_tiles = (p.total + p.tile - 1) / p.tile, step = gridDim.x * ET_GROUPS;

@@ -31,6 +31,8 @@ namespace csa2 {
 // feed faster anyway (4 KB of operands in 32 cycles); a single 128-key tile,
 // filled, multiplied and filled again, took twice as long.
 constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 16;
+constexpr int PA_PART = 4 * PA_ROWS / PA_SM_WARPS;  // query rows of a softmax warp
+constexpr int PA_COLS = PA_PART / 4;                // and of a thread
 constexpr int PA_MMA_WARP = PA_DQ_WARPS + PA_SM_WARPS;
 constexpr int PA_NT = 32 * (PA_MMA_WARP + 3);
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
@@ -99,7 +101,7 @@ struct PaSmem {
   int abort;
   PaRun run;
 };
-constexpr size_t PA_SMEM = sizeof(PaSmem) + 1024;
+constexpr size_t PA_SMEM = sizeof(PaSmem);
 static_assert(PA_SMEM <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ uint32_t pa_h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -402,9 +404,10 @@ __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& r
 }
 
 __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  PaSmem& s = *reinterpret_cast<PaSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                         ~uintptr_t(1023));
+  // declared with its alignment rather than rounded up to it: a rounded pointer is
+  // a generic one, whose 64-bit addresses cost the inner loops a third of their time
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PaSmem& s = *reinterpret_cast<PaSmem*>(smem_raw);
   const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
   pdl_launch_dependents();
   if (t == 0) {
@@ -574,23 +577,23 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     }
   } else if (warp < PA_MMA_WARP) {
     // --------------------------------------------------------- softmax
-    // Warp (quad, part): keys 16 quad + [0, 16), query rows 16 part + [0, 16).  An
+    // Warp (quad, part): keys 16 quad + [0, 16), query rows PA_PART part + [0, PA_PART).  An
     // M = 64 accumulator has its rows in lanes 0..15 of each TMEM quarter; read as
     // 16 x 256 bits, a thread holds keys lane / 4 and lane / 4 + 8 by columns
-    // 8 n + 2 (lane % 4) + {0, 1}, n < 2.
+    // 8 n + 2 (lane % 4) + {0, 1}, n < PA_PART / 8.
     const int w = warp - PA_DQ_WARPS, quad = w & 3, part = w >> 2;
     const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-    const int c0 = 16 * part + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
+    const int c0 = PA_PART * part + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
     const PaRun& run = s.run;
     for (;;) {
       bar_sync<PA_NT>(BAR_RUN);
       if (!run.valid) break;
       pa_queries(p, run, s, w, lane);
       bar_sync<Q_THREADS>(BAR_Q);
-      const bool active = 16 * part < run.n_rows;  // per warp
-      float scl[4], m[4], l[4];
+      const bool active = PA_PART * part < run.n_rows;  // per warp
+      float scl[PA_COLS], m[PA_COLS], l[PA_COLS];
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
+      for (int j = 0; j < PA_COLS; j++) {
         const int c = c0 + 8 * (j >> 1) + (j & 1);
         scl[j] = c < run.n_rows ? s.scl[c] : 0.0f;
         m[j] = PA_NONE;
@@ -601,29 +604,30 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         const bool win = run.own && kt >= run.own_tiles;
         const int first = win ? run.win_lo + (kt - run.own_tiles) * PA_KEYS
                               : run.first_pos + kt * PA_KEYS;
+        // the keys' flags are there before S^T is
+        if (!pa_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
+        const uint32_t f0 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0]);
+        const uint32_t f1 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0 + 8]);
+        const bool plain = first >= s.lo_max[win] && first + PA_KEYS <= s.hi_min[win] &&
+                           __all_sync(0xffffffffu, (f0 | f1) == 0);
         if (!pa_wait(&s.s_full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
-        pa_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort);  // (complete) the keys' flags
         __syncwarp();
         tc_fence_after();
         if (active) {
-          const uint32_t f0 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0]);
-          const uint32_t f1 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0 + 8]);
-          const bool plain = first >= s.lo_max[win] && first + PA_KEYS <= s.hi_min[win] &&
-                             __all_sync(0xffffffffu, (f0 | f1) == 0);
           // x[4 n + 2 k + e]: key k0 + 8 k, row c0 + 8 n + e: the logit less f times
           // the row's reference
-          auto logits = [&](float f, float(&x)[8]) {
-            uint32_t acc[8];
-            tmem_ld_16x256b_x2(tmem + lane_base + PA_S_COL + PA_ROWS * (i & 1) + 16 * part, acc);
+          auto logits = [&](float f, float(&x)[2 * PA_COLS]) {
+            uint32_t acc[2 * PA_COLS];
+            tmem_ld_16x256b(tmem + lane_base + PA_S_COL + PA_ROWS * (i & 1) + PA_PART * part, acc);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
+            for (int j = 0; j < 2 * PA_COLS; j++) {
               const int c = 2 * (j >> 2) + (j & 1);
               x[j] = fmaf(__uint_as_float(acc[j]), scl[c], f * m[c]);
             }
             if (!plain) {
 #pragma unroll
-              for (int j = 0; j < 8; j++) {
+              for (int j = 0; j < 2 * PA_COLS; j++) {
                 const int c = c0 + 8 * (j >> 2) + (j & 1), key = first + k0 + 8 * ((j >> 1) & 1);
                 const uint32_t bad = (j >> 1) & 1 ? f1 : f0;
                 const bool see = !(bad & 1u) && key >= s.lo[win][c] && key < s.hi[win][c];
@@ -631,17 +635,17 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
               }
             }
           };
-          float x[8];
+          float x[2 * PA_COLS];
           logits(-1.0f, x);
           float over = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) over = fmaxf(over, fmaxf(x[j], x[j + 1]));
+          for (int j = 0; j < 2 * PA_COLS; j += 2) over = fmaxf(over, fmaxf(x[j], x[j + 1]));
           if (bar_or_128(1 + part, over > PA_SHIFT + PA_SLACK)) {
             // some logit is far above its reference: raise the references to the
             // rows' maxima and scale what was summed
             logits(0.0f, x);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
+            for (int j = 0; j < PA_COLS; j++) {
               float mx = fmaxf(x[4 * (j >> 1) + (j & 1)], x[4 * (j >> 1) + 2 + (j & 1)]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1)
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             }
             bar_or_128(1 + part, false);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
+            for (int j = 0; j < PA_COLS; j++) {
               const int c = c0 + 8 * (j >> 1) + (j & 1);
               const float mx = fmaxf(fmaxf(s.red[0][c], s.red[1][c]), fmaxf(s.red[2][c], s.red[3][c]));
               const float top = fmaxf(m[j], mx - PA_SHIFT), f = ex2(m[j] - top);
@@ -665,14 +669,15 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
-              for (int cb = 0; cb < 4; cb++) {  // channel blocks
-                const uint32_t at = tmem + lane_base + 64 * cb + 16 * part;
+              for (int g = 0; g < 4 * PA_PART / 16; g++) {  // channel block, 16 rows
+                const int c = PA_PART * part + 16 * (g >> 2);
+                const uint32_t at = tmem + lane_base + 64 * (g & 3) + c;
                 uint32_t o[16];
                 tmem_ld_x16(at, o);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; j++)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * s.fac[16 * part + j]);
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * s.fac[c + j]);
                 tmem_st_x16(at, o);
               }
               tmem_st_wait();
@@ -681,12 +686,12 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
           }
           uint8_t* dst = s.p[i & 1] + k0 * 128 + 4 * (lane & 3);
 #pragma unroll
-          for (int n = 0; n < 2; n++) {
+          for (int n = 0; n < PA_COLS / 2; n++) {
             const float p0 = ex2(x[4 * n]), p1 = ex2(x[4 * n + 1]);
             const float p2 = ex2(x[4 * n + 2]), p3 = ex2(x[4 * n + 3]);
             l[2 * n] += p0 + p2;
             l[2 * n + 1] += p1 + p3;
-            const uint32_t at = (uint32_t)((2 * part + n) ^ (k0 & 7)) << 4;  // (k0 + 8 alike)
+            const uint32_t at = (uint32_t)((PA_PART / 8 * part + n) ^ (k0 & 7)) << 4;  // (k0 + 8 alike)
             *reinterpret_cast<uint32_t*>(dst + at) = pa_h2u(__floats2half2_rn(p0, p1));
             *reinterpret_cast<uint32_t*>(dst + 1024 + at) = pa_h2u(__floats2half2_rn(p2, p3));
           }
@@ -703,7 +708,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       tc_fence_after();
       if (active) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < PA_COLS; j++) {
           float v = l[j];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -714,18 +719,20 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
           }
         }
         bar_or_128(1 + part, false);
-        const int c = 16 * part + lane;
-        if (quad == 0 && lane < 16) {
+        const int c = PA_PART * part + lane;
+        if (quad == 0 && lane < PA_PART && c < run.n_rows) {
           p.part_ml[2 * (run.slot + c)] = s.fac[c];
           p.part_ml[2 * (run.slot + c) + 1] =
               (s.red[0][c] + s.red[1][c]) + (s.red[2][c] + s.red[3][c]);
         }
 #pragma unroll 2
-        for (int cb = 0; cb < 4; cb++) {
+        for (int g = 0; g < 4 * PA_PART / 16; g++) {  // channel block, 16 rows
+          const int r0 = PA_PART * part + 16 * (g >> 2);
+          if (r0 >= run.n_rows) continue;
           uint32_t o[16];
-          tmem_ld_x16(tmem + lane_base + 64 * cb + 16 * part, o);
+          tmem_ld_x16(tmem + lane_base + 64 * (g & 3) + r0, o);
           tmem_ld_wait();
-          float* dst = p.part_o + (run.slot + 16 * part) * CSA2_D + 128 * cb +
+          float* dst = p.part_o + (run.slot + r0) * CSA2_D + 128 * (g & 3) +
                        pa_channel(32 * quad + lane);
 #pragma unroll
           for (int j = 0; j < 16; j++) dst[j * CSA2_D] = __uint_as_float(o[j]) * PA_TILE_SCALE;
@@ -812,23 +819,26 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   }
 }
 
-// One CTA per query row: out = sum_i w_i O_i / sum_i w_i l_i over the row's
-// partials, w_i = 2^(m_i - max m).  Four groups of 128 threads (four channels
-// each) take every fourth partial; their sums join in a fixed order.
+// out = sum_i w_i O_i / sum_i w_i l_i over a row's partials, w_i = 2^(m_i - max m).
+// All heads of a query share the list of partials.  A CTA takes HEADS heads of one
+// query: all 16 where the queries alone fill the GPU (a CTA's look at the plan
+// costs more than a row's sum), else one, its partials dealt to four groups of 128
+// threads (four channels each) whose sums join in a fixed order.
 constexpr int PM_NT = 512;
+template <int HEADS>
 __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams p) {
   __shared__ int64_t slot[2 * PA_MAX_GRID];
-  __shared__ float w[2 * PA_MAX_GRID];
+  __shared__ float w[2 * PA_MAX_GRID][HEADS];
   __shared__ int sums[2];
-  __shared__ float red[PM_NT / 32];
-  __shared__ float total_l;
+  __shared__ float inv[HEADS];
   __shared__ float4 acc_s[3][128];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row = blockIdx.x;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int qi = blockIdx.x / (CSA2_H / HEADS), h0 = blockIdx.x % (CSA2_H / HEADS) * HEADS;
   pdl_launch_dependents();
   pdl_wait();
   if (t < 2) sums[t] = 0;
   __syncthreads();
-  const int qi = row / CSA2_H, b = qi / p.nq, tq = qi - b * p.nq;
+  const int b = qi / p.nq, tq = qi - b * p.nq;
   PaPlan pl = pa_plan(p);
   int before = 0, all = 0;
   for (int i = t; i < p.batch; i += PM_NT) {
@@ -838,7 +848,7 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
-  if (lane == 0) {
+  if (lane == 0 && (all | before) != 0) {
     atomicAdd(&sums[0], all);  // whole numbers: any order gives the same sum
     atomicAdd(&sums[1], before);
   }
@@ -846,8 +856,8 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   pl.finish(sums[0]);
   const int kts = pa_own_line(p, pl, p.n_rows[b]);
 
-  // ---- the row's partials: shared segment, then own segment
-  const int qb = tq / PA_QB, seg = row / PA_ROWS, oseg = b * pl.q_blocks + qb;
+  // ---- the query's partials (row of head 0): shared segment, then own segment
+  const int qb = tq / PA_QB, row0 = qi * CSA2_H, seg = row0 / PA_ROWS, oseg = b * pl.q_blocks + qb;
   const int64_t ts[2] = {(int64_t)seg * pl.prefix_tiles,
                          pl.shared + (int64_t)sums[1] * pl.q_blocks + (int64_t)qb * kts};
   const int64_t te[2] = {ts[0] + pl.prefix_tiles, ts[1] + kts};
@@ -860,74 +870,82 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
     }
   }
   const int n = count[0] + count[1];
-  float m = -INFINITY, l = 0.0f;
-  int64_t at = 0;
   if (t < n) {  // n <= 2 * PA_MAX_GRID <= PM_NT
     const int k = t < count[0] ? 0 : 1, c = first[k] + (k ? t - count[0] : t);
     const int64_t a = max(pl.tile_at(c), ts[k] + (k ? PA_SEG : 0)), z = min(pl.tile_at(c + 1), te[k]);
-    if (a < z) {
-      at = k ? pl.own_slot(oseg, c) + (tq - qb * PA_QB) * CSA2_H + row % CSA2_H
-             : pl.shared_slot(seg, c) + row % PA_ROWS;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-      if (ml.y > 0.0f || ml.y != ml.y) {  // a NaN sum stays one
-        m = ml.x;
-        l = ml.y;
+    slot[t] = a >= z ? -1 : k ? pl.own_slot(oseg, c) + (tq - qb * PA_QB) * CSA2_H
+                              : pl.shared_slot(seg, c) + row0 % PA_ROWS;
+  }
+  __syncthreads();
+  // ---- weights: a warp per head (a NaN sum stays one)
+  if (warp < HEADS) {
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) {
+      float m = -INFINITY;
+      if (slot[i] >= 0) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot[i] + h0 + warp));
+        if (ml.y > 0.0f || ml.y != ml.y) m = ml.x;
+      }
+      w[i][warp] = m;
+      M = fmaxf(M, m);
+    }
+    M = warp_max_f32(M);
+    float sum = 0.0f;
+    for (int i = lane; i < n; i += 32) {
+      const float wt = w[i][warp] == -INFINITY ? 0.0f : exp2f(w[i][warp] - M);
+      w[i][warp] = wt;
+      if (slot[i] >= 0 && M != -INFINITY) {
+        const float l = p.part_ml[2 * (slot[i] + h0 + warp) + 1];
+        if (wt != 0.0f || l != l) sum += wt * l;
       }
     }
-  }
-  {
-    const float v = warp_max_f32(m);
-    if (lane == 0) red[warp] = v;
-  }
-  __syncthreads();
-  float M = red[0];
 #pragma unroll
-  for (int i = 1; i < PM_NT / 32; i++) M = fmaxf(M, red[i]);
-  const float wt = m == -INFINITY ? 0.0f : exp2f(m - M);
-  if (t < n) {
-    slot[t] = at;
-    w[t] = wt;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) inv[warp] = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
-  float sl = wt * l;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sl += __shfl_xor_sync(0xffffffffu, sl, o);
   __syncthreads();
-  if (lane == 0) red[warp] = sl;
-  __syncthreads();
-  if (t == 0) {
-    float v = 0.0f;
-    for (int i = 0; i < PM_NT / 32; i++) v += red[i];
-    total_l = v;
-  }
-  // ---- the weighted sum
+  // ---- the weighted sums
   const int g = t >> 7, ch = 4 * (t & 127);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = g; i < n; i += 4) {
-    if (w[i] == 0.0f) continue;
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot[i] * CSA2_D + ch);
-    acc.x = fmaf(w[i], v.x, acc.x);
-    acc.y = fmaf(w[i], v.y, acc.y);
-    acc.z = fmaf(w[i], v.z, acc.z);
-    acc.w = fmaf(w[i], v.w, acc.w);
-  }
-  if (g > 0) acc_s[g - 1][t & 127] = acc;
-  __syncthreads();
-  if (g == 0) {
-#pragma unroll
-    for (int k = 0; k < 3; k++) {
-      const float4 v = acc_s[k][t];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-    }
-    const float tl = total_l;
-    const float inv = tl == 0.0f ? 0.0f : 1.0f / tl;
-    const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 o1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + (int64_t)row * CSA2_D + ch) =
+  auto store = [&](int h, float4 acc) {
+    const float f = inv[h];
+    const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    const __nv_bfloat162 o1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(p.out + (int64_t)(row0 + h0 + h) * CSA2_D + ch) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+  };
+  auto add = [&](int h, int i, float4& acc) {
+    const float wt = w[i][h];
+    if (wt == 0.0f) return;
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot[i] + h0 + h) * CSA2_D + ch);
+    acc.x = fmaf(wt, v.x, acc.x);
+    acc.y = fmaf(wt, v.y, acc.y);
+    acc.z = fmaf(wt, v.z, acc.z);
+    acc.w = fmaf(wt, v.w, acc.w);
+  };
+  if (HEADS > 1) {
+#pragma unroll 2
+    for (int h = g; h < HEADS; h += 4) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < n; i++) add(h, i, acc);
+      store(h, acc);
+    }
+  } else {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = g; i < n; i += 4) add(0, i, acc);
+    if (g > 0) acc_s[g - 1][t & 127] = acc;
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+      for (int k = 0; k < 3; k++) {
+        const float4 v = acc_s[k][t];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      store(0, acc);
+    }
   }
 }
 
@@ -965,11 +983,14 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t st) {
   cfg.numAttrs = 1;
   trace_mark("prefix_attn", st);
   if ((e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel, p)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(p.batch * p.nq * CSA2_H);
+  const int queries = p.batch * p.nq;
+  const bool whole = queries >= num_sms();
+  cfg.gridDim = dim3(whole ? queries : queries * CSA2_H);
   cfg.blockDim = dim3(PM_NT);
   cfg.dynamicSmemBytes = 0;
   trace_mark("prefix_merge", st);
-  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel, p);
+  return whole ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<CSA2_H>, p)
+               : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<1>, p);
 }
 
 }  // namespace csa2
