@@ -97,9 +97,10 @@ struct PaSmem {
   int wsum[32];
   uint64_t full[2], empty[2];    // tile buffer: written, multiplied
   uint64_t s_full[2], p_full[2];
+  uint64_t run_full[2], run_empty[2];  // run planned, done with by every role
   uint32_t tmem_base;
   int abort;
-  PaRun run;
+  PaRun run[2];
 };
 constexpr size_t PA_SMEM = sizeof(PaSmem);
 static_assert(PA_SMEM <= 232448, "shared memory of one CTA");
@@ -325,12 +326,12 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
 __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& run, PaSmem& s,
                                            int warp, int lane) {
       // Q' = Q * 2^e in fp16, max |Q'| of a row in [2^14, 2^15): one warp per row,
-  // 16 channels per lane, two rows' loads in flight
+  // 16 channels per lane, four rows' loads in flight
 #pragma unroll 1
-  for (int h0 = warp; h0 < run.n_rows; h0 += 2 * PA_SM_WARPS) {
-    uint4 v[2][2];
+  for (int h0 = warp; h0 < run.n_rows; h0 += 4 * PA_SM_WARPS) {
+    uint4 v[4][2];
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
+    for (int u = 0; u < 4; u++) {
       const int h = min(h0 + u * PA_SM_WARPS, run.n_rows - 1);
       const uint4* src =
           reinterpret_cast<const uint4*>(p.q + (int64_t)(run.row0 + h) * CSA2_D) + 2 * lane;
@@ -338,7 +339,7 @@ __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& r
       v[u][1] = __ldg(src + 1);
     }
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
+    for (int u = 0; u < 4; u++) {
       const int h = h0 + u * PA_SM_WARPS;
       if (h >= run.n_rows) break;
       uint32_t mx = 0u;
@@ -417,6 +418,8 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       mbar_init(&s.empty[i], 1);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], PA_SM_WARPS);
+      mbar_init(&s.run_full[i], 1);
+      mbar_init(&s.run_empty[i], PA_MMA_WARP + 2);
     }
     fence_mbar_init();
     s.abort = 0;
@@ -467,12 +470,25 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   pl.finish(s.cum[p.batch]);
   const uint32_t tmem = s.tmem_base;
 
-  // Per run of tiles: BAR_RUN (the run is known), BAR_Q (its queries are in
-  // shared memory; softmax and MMA warps), the tiles, BAR_RUN (all is done).
+  // The runs of tiles, planned one ahead; a role goes on to the next run when its
+  // part of this one is done (the tiles' barriers keep it from running away).
   // Tile i of the CTA uses buffers i & 1; their barriers' phase is (i >> 1) & 1.
-  // (1 to 4: the softmax warps of 16 rows, 5: all softmax warps)
-  constexpr int BAR_RUN = 6, BAR_Q = 7;
-  constexpr int Q_THREADS = 32 * (PA_SM_WARPS + 2);
+  // Named barriers 1 to 4: the softmax warps of 16 rows, 5: all softmax warps,
+  // BAR_Q: a run's queries are in shared memory (softmax and MMA warps).
+  constexpr int BAR_Q = 6, Q_THREADS = 32 * (PA_SM_WARPS + 2);
+  uint32_t n_run = 0;
+  // Waits for the next run's plan.  The planner always gives one (after an expired
+  // wait anywhere: that there is none), and every role goes by its `valid` alone, so
+  // all reach the same barriers.
+  auto next_run = [&]() -> const PaRun& {
+    const uint32_t k = n_run++;
+    mbar_wait(&s.run_full[k & 1], (k >> 1) & 1, nullptr, 2 * kWaitCycles);
+    return s.run[k & 1];
+  };
+  auto done_run = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.run_empty[(n_run - 1) & 1]);
+  };
   uint32_t i = 0;
   if (warp < PA_DQ_WARPS) {
     // ------------------------------------------------ key tiles to fp16
@@ -483,8 +499,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     // while this one's wait for a free buffer and are turned.
     const int seg = lane >> 3, r = 8 * warp + (lane & 7), sw = lane & 7, cc = 4 * (seg & 1);
     for (;;) {
-      bar_sync<PA_NT>(BAR_RUN);
-      const PaRun& run = s.run;
+      const PaRun& run = next_run();
       if (!run.valid) break;
       const int kt_end = run.kt_end, kt_cache = run.kt_cache;
       uint4 v[4], nv[4];       // by block: this tile's codes, the next one's
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[i & 1]);
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      done_run();
     }
   } else if (warp < PA_MMA_WARP) {
     // --------------------------------------------------------- softmax
@@ -584,10 +599,10 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     const int w = warp - PA_DQ_WARPS, quad = w & 3, part = w >> 2;
     const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
     const int c0 = PA_PART * part + 2 * (lane & 3), k0 = 16 * quad + (lane >> 2);
-    const PaRun& run = s.run;
     for (;;) {
-      bar_sync<PA_NT>(BAR_RUN);
+      const PaRun& run = next_run();
       if (!run.valid) break;
+      bar_sync<32 * PA_SM_WARPS>(5);  // all have left the last run
       pa_queries(p, run, s, w, lane);
       bar_sync<Q_THREADS>(BAR_Q);
       const bool active = PA_PART * part < run.n_rows;  // per warp
@@ -739,7 +754,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         }
         tc_fence_before();
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      done_run();
     }
   } else {
     // ------------------------------------------------------ the products
@@ -750,23 +765,28 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     if (warp == PA_MMA_WARP + 2) {
       int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
       const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
-      for (bool valid = true; valid;) {
+      for (bool valid = true; valid; n_run++) {
         PaRun r;
         do {  // skips what holds empty tiles only
           r = pa_next_run(p, pl, s.cum, tile, tile_end, s.abort != 0);
           if (r.valid) tile += r.line;
         } while (r.valid && r.kt_end <= r.kt);
-        if (lane == 0) s.run = r;
         valid = r.valid;
-        bar_sync<PA_NT>(BAR_RUN);
-        if (valid) bar_sync<PA_NT>(BAR_RUN);
+        const uint32_t k = n_run;
+        if (k >= 2 && !pa_wait(&s.run_empty[k & 1], ((k >> 1) - 1) & 1, &s.abort)) s.abort = 1;
+        valid = __all_sync(0xffffffffu, valid && !s.abort);
+        if (lane == 0) {
+          if (valid) s.run[k & 1] = r;
+          s.run[k & 1].valid = valid;  // (alone: a role may still be at the run before last)
+          mbar_arrive(&s.run_full[k & 1]);
+        }
       }
     }
     while (warp <= PA_MMA_WARP + 1) {
-      bar_sync<PA_NT>(BAR_RUN);
-      if (!s.run.valid) break;
-      const uint32_t begin = i, end = i + (uint32_t)(s.run.kt_end - s.run.kt);
-      const uint32_t id = pa_idesc(s.run.n_rows, warp != PA_MMA_WARP);
+      const PaRun& run = next_run();
+      if (!run.valid) break;
+      const uint32_t begin = i, end = i + (uint32_t)(run.kt_end - run.kt);
+      const uint32_t id = pa_idesc(run.n_rows, warp != PA_MMA_WARP);
       bar_sync<Q_THREADS>(BAR_Q);
       tc_fence_after();
       const bool leader = elect_one();
@@ -807,12 +827,12 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
           __syncwarp();
         }
       }
-      bar_sync<PA_NT>(BAR_RUN);
+      done_run();
     }
   }
-  if (s.abort && t == 0) set_status(p.status, ST_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  if (s.abort && t == 0) set_status(p.status, ST_TIMEOUT);
   if (warp == PA_MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, PA_TMEM_COLS);

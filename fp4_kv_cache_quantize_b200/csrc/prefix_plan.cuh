@@ -22,10 +22,10 @@ constexpr int PA_KEYS = 64;      // keys per tile: the MMA's M
 constexpr int PA_ROWS = 64;      // query rows per tile: the MMA's N
 constexpr int PA_QB = PA_ROWS / CSA2_H;  // queries per row block
 constexpr int PA_MAX_GRID = 192;
-constexpr int PA_SEG = 3;
+constexpr int PA_SEG = 6;
 
 // What a tile of n rows costs, relative to others.
-__host__ __device__ inline int pa_cost(int n_rows) { return 12 + n_rows / 16; }
+__host__ __device__ inline int pa_cost(int n_rows) { return 14 + n_rows / 32; }
 
 struct PaPlan {
   int row_blocks;   // blocks of 64 rows over the whole batch
