@@ -23,18 +23,36 @@
 
 namespace csa2 {
 
+// What bounds it: at 64 query rows a 64-key tile costs 1,792 cycles of tensor core
+// (32 S^T steps of 32 cycles, 16 O^T steps of 48), about 2,840 of shared memory's
+// data path (the products read K, V, Q' and P, the warps write K and P) and 2,200 issue
+// slots on each scheduler.  They overlap to 3,550 cycles per tile: shared memory's
+// path is busy 2/3 of the time, the schedulers 55%, the tensor core 40%.
+//   128K-row prefix, 64 sequences (1,024 rows): 475 us, 0.58 PFLOP/s
+//   1M-row prefix, 4 sequences (64 rows): 238 us, 1.27 TB/s of cache rows
+//   2K-row prefix, 4 sequences: 22 us (a CTA's one tile takes 18,000 cycles from its
+//   start to its partial; the merge 4 us more)
+//
 // Roles of a CTA: eight warps turn key tiles into fp16, sixteen run the softmax,
 // one thread issues the S^T products and one the O^T products, one warp works out
 // which tiles come next.  Key tiles are 64 keys so that two fit next to the
 // queries: while one is multiplied, the next is written.  S^T then is an M = 64
 // product at half the tensor core's rate, but one that shared memory could not
 // feed faster anyway (4 KB of operands in 32 cycles); a single 128-key tile,
-// filled, multiplied and filled again, took twice as long.
+// filled, multiplied and filled again, took twice as long.  Sixteen dequantising
+// and eight softmax warps, with registers moved between them, took 463 us instead
+// of 475 at 1,024 rows but 519 instead of 500 at 512 rows with queries of their own.
 constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 16;
 constexpr int PA_PART = 4 * PA_ROWS / PA_SM_WARPS;  // query rows of a softmax warp
 constexpr int PA_COLS = PA_PART / 4;                // and of a thread
 constexpr int PA_MMA_WARP = PA_DQ_WARPS + PA_SM_WARPS;
 constexpr int PA_NT = 32 * (PA_MMA_WARP + 3);
+// A tile is written, multiplied and freed in parts of 256 channels: S^T begins with
+// the first part, and the first part is filled again while the second is still in
+// the O^T products (a million-row prefix 247 -> 238 us; in one piece the four steps
+// of a tile take 6,500 cycles one after the other.  Four parts cost more fences and
+// waits than they save: 293).
+constexpr int PA_PARTS = 2;
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
 constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
 constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
@@ -95,7 +113,7 @@ struct PaSmem {
   float red[4][PA_ROWS];
   int cum[CSA2_PREFIX_MAX_BATCH + 1];         // own tiles on the line of sequences < b
   int wsum[32];
-  uint64_t full[2], empty[2];    // tile buffer: written, multiplied
+  uint64_t full[2][PA_PARTS], empty[2][PA_PARTS];  // part of a tile: written, multiplied
   uint64_t s_full[2], p_full[2];
   uint64_t run_full[2], run_empty[2];  // run planned, done with by every role
   uint32_t tmem_base;
@@ -325,7 +343,7 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
 // The softmax warps bring a run's queries and limits into shared memory.
 __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& run, PaSmem& s,
                                            int warp, int lane) {
-      // Q' = Q * 2^e in fp16, max |Q'| of a row in [2^14, 2^15): one warp per row,
+  // Q' = Q * 2^e in fp16, max |Q'| of a row in [2^14, 2^15): one warp per row,
   // 16 channels per lane, four rows' loads in flight
 #pragma unroll 1
   for (int h0 = warp; h0 < run.n_rows; h0 += 4 * PA_SM_WARPS) {
@@ -414,8 +432,11 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   if (t == 0) {
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      mbar_init(&s.full[i], PA_DQ_WARPS);
-      mbar_init(&s.empty[i], 1);
+#pragma unroll
+      for (int c = 0; c < PA_PARTS; c++) {
+        mbar_init(&s.full[i][c], PA_DQ_WARPS);
+        mbar_init(&s.empty[i][c], 1);
+      }
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], PA_SM_WARPS);
       mbar_init(&s.run_full[i], 1);
@@ -498,6 +519,19 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     // swizzle gives them different banks.  The next tile's codes are on their way
     // while this one's wait for a free buffer and are turned.
     const int seg = lane >> 3, r = 8 * warp + (lane & 7), sw = lane & 7, cc = 4 * (seg & 1);
+    // before and after the tile's 128-channel block b is written
+    auto begin_part = [&](int b) {
+      constexpr int N = 4 / PA_PARTS;
+      if (b % N == 0 && i >= 2)
+        pa_wait(&s.empty[i & 1][b / N], ((i >> 1) - 1) & 1, &s.abort);
+    };
+    auto end_part = [&](int b) {
+      constexpr int N = 4 / PA_PARTS;
+      if (b % N != N - 1) return;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.full[i & 1][b / N]);
+    };
     for (;;) {
       const PaRun& run = next_run();
       if (!run.valid) break;
@@ -540,10 +574,10 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         const bool nan = has_nan(sc[0] | (sc[1] << 16)) || has_nan(sc[2] | (sc[3] << 16));
         const bool zero = row < 0 || nan;
         uint8_t* dst = s.tile[i & 1] + (seg >> 1) * PA_KB + r * 128;
-        if (i >= 2) pa_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
-        s.key[i & 1][r][seg] = (uint8_t)(row < 0 ? 1 : (nan ? 2 : 0));
 #pragma unroll
         for (int b = 0; b < 4; b++) {
+          begin_part(b);
+          if (b == 0) s.key[i & 1][r][seg] = (uint8_t)(row < 0 ? 1 : (nan ? 2 : 0));
           if (!zero) {
             pa_put_fp4(dst + 2 * b * PA_KB, sw, cc, v[b], sc[b]);
           } else {
@@ -552,10 +586,8 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
               *reinterpret_cast<uint4*>(dst + 2 * b * PA_KB + (((cc + c) ^ sw) << 4)) =
                   make_uint4(0, 0, 0, 0);
           }
+          end_part(b);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.full[i & 1]);
       }
 #pragma unroll 1
       for (; kt < kt_end; kt++, i++) {  // window tiles
@@ -574,19 +606,17 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             nan |= has_nan(a[b].x) || has_nan(a[b].y) || has_nan(a[b].z) || has_nan(a[b].w);
         }
         uint8_t* dst = s.tile[i & 1] + (seg >> 1) * PA_KB + r * 128;
-        if (i >= 2) pa_wait(&s.empty[i & 1], ((i >> 1) - 1) & 1, &s.abort);
-        s.key[i & 1][r][seg] = (uint8_t)(w >= run.n_win ? 1 : (nan ? 2 : 0));
 #pragma unroll
         for (int b = 0; b < 8; b++) {
+          if (b % 2 == 0) begin_part(b / 2);
+          if (b == 0) s.key[i & 1][r][seg] = (uint8_t)(w >= run.n_win ? 1 : (nan ? 2 : 0));
           if (nan) a[b] = make_uint4(0u, 0u, 0u, 0u);
           uint8_t* d = dst + 2 * (b >> 1) * PA_KB;
           const int c = cc + 2 * (b & 1);
           *reinterpret_cast<uint4*>(d + ((c ^ sw) << 4)) = pa_e4m3x8(a[b].x, a[b].y);
           *reinterpret_cast<uint4*>(d + (((c + 1) ^ sw) << 4)) = pa_e4m3x8(a[b].z, a[b].w);
+          if (b % 2 == 1) end_part(b / 2);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.full[i & 1]);
       }
       done_run();
     }
@@ -620,7 +650,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         const int first = win ? run.win_lo + (kt - run.own_tiles) * PA_KEYS
                               : run.first_pos + kt * PA_KEYS;
         // the keys' flags are there before S^T is
-        if (!pa_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
+        if (!pa_wait(&s.full[i & 1][0], (i >> 1) & 1, &s.abort)) s.abort = 1;
         const uint32_t f0 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0]);
         const uint32_t f1 = *reinterpret_cast<const uint32_t*>(s.key[i & 1][k0 + 8]);
         const bool plain = first >= s.lo_max[win] && first + PA_KEYS <= s.hi_min[win] &&
@@ -680,7 +710,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             bar_or_128(1 + part, false);
             if (kt != run.kt) {
               // the products up to the last tile's are in O
-              if (!pa_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
+              if (!pa_wait(&s.empty[(i - 1) & 1][PA_PARTS - 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -718,7 +748,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       }
       // ---- the run's partial: O [row][channel], (max, sum) per row.  The last
       // tile's commit covers every product.
-      if (!pa_wait(&s.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
+      if (!pa_wait(&s.empty[(i - 1) & 1][PA_PARTS - 1], ((i - 1) >> 1) & 1, &s.abort)) s.abort = 1;
       __syncwarp();
       tc_fence_after();
       if (active) {
@@ -794,19 +824,24 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         const PaDesc qd(sdesc_k128(smem_u32(s.q))), kd(sdesc_k128(smem_u32(s.tile[0])));
 #pragma unroll 1
         for (; i < end; i++) {
-          if (!pa_wait(&s.full[i & 1], (i >> 1) & 1, &s.abort)) s.abort = 1;
-          __syncwarp();
-          tc_fence_after();
-          if (leader) {  // S^T = K Q'^T: K = 512, eight chunks of four steps
-            const uint32_t a = (i & 1) * ((8 * PA_KB) >> 4);
-            const uint32_t d = tmem + PA_S_COL + PA_ROWS * (i & 1);
+          const uint32_t a = (i & 1) * ((8 * PA_KB) >> 4);
+          const uint32_t d = tmem + PA_S_COL + PA_ROWS * (i & 1);
 #pragma unroll
-            for (uint32_t k = 0; k < 32; k++)
-              pa_umma(d, kd, a + (((k >> 2) * PA_KB) >> 4) + 2 * (k & 3), qd,
-                      (((k >> 2) * PA_QKB) >> 4) + 2 * (k & 3), id, k != 0);
-            umma_commit(&s.s_full[i & 1]);
+          for (uint32_t c = 0; c < PA_PARTS; c++) {  // S^T = K Q'^T: K = 512
+            if (!pa_wait(&s.full[i & 1][c], (i >> 1) & 1, &s.abort)) s.abort = 1;
+            __syncwarp();
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (uint32_t j = 0; j < 32 / PA_PARTS; j++) {
+                const uint32_t k = c * (32 / PA_PARTS) + j;
+                pa_umma(d, kd, a + (((k >> 2) * PA_KB) >> 4) + 2 * (k & 3), qd,
+                        (((k >> 2) * PA_QKB) >> 4) + 2 * (k & 3), id, k != 0);
+              }
+              if (c == PA_PARTS - 1) umma_commit(&s.s_full[i & 1]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       } else {
         const PaDesc pd(sdesc_mn128(smem_u32(s.p[0]), PA_KEYS * 128, 1024));
@@ -819,10 +854,13 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
           if (leader) {  // O^T += V^T P^T: K = 64 keys in four steps, four channel blocks
             const uint32_t a = (i & 1) * ((8 * PA_KB) >> 4), b = (i & 1) * ((PA_KEYS * 128) >> 4);
 #pragma unroll
-            for (uint32_t k = 0; k < 16; k++)
-              pa_umma(tmem + 64 * (k & 3), vd, a + (((k & 3) * 2 * PA_KB + (k >> 2) * 2048) >> 4), pd,
-                      b + (((k >> 2) * 2048) >> 4), id, i != begin || k >= 4);
-            umma_commit(&s.empty[i & 1]);
+            for (uint32_t k = 0; k < 16; k++) {
+              const uint32_t c = k >> 2, j = k & 3;  // channel block, 16 keys
+              pa_umma(tmem + 64 * c, vd, a + ((c * 2 * PA_KB + j * 2048) >> 4), pd,
+                      b + ((j * 2048) >> 4), id, i != begin || j != 0);
+              if (k % (16 / PA_PARTS) == 16 / PA_PARTS - 1)
+                umma_commit(&s.empty[i & 1][c * PA_PARTS / 4]);
+            }
           }
           __syncwarp();
         }
