@@ -28,10 +28,10 @@ namespace csa2 {
 // data path (the products read K, V, Q' and P, the warps write K and P) and 2,200 issue
 // slots on each scheduler.  They overlap to 3,550 cycles per tile: shared memory's
 // path is busy 2/3 of the time, the schedulers 55%, the tensor core 40%.
-//   128K-row prefix, 64 sequences (1,024 rows): 475 us, 0.58 PFLOP/s
-//   1M-row prefix, 4 sequences (64 rows): 238 us, 1.27 TB/s of cache rows
-//   2K-row prefix, 4 sequences: 22 us (a CTA's one tile takes 18,000 cycles from its
-//   start to its partial; the merge 4 us more)
+//   128K-row prefix, 64 sequences (1,024 rows): 478 us, 0.58 PFLOP/s
+//   1M-row prefix, 4 sequences (64 rows): 226 us, 1.34 TB/s of cache rows
+//   2K-row prefix, 4 sequences: 18 us, the latencies of one tile a CTA (lengths,
+//   plan, page, rows, products, softmax, partial) and of the merge
 //
 // Roles of a CTA: eight warps turn key tiles into fp16, sixteen run the softmax,
 // one thread issues the S^T products and one the O^T products, one warp works out
@@ -158,6 +158,14 @@ __device__ __forceinline__ uint4 ld_now_v4(const void* a) {
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(a));
+  return v;
+}
+__device__ __forceinline__ float4 ld_now_f4(const float* a) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t ld_now_u16(const void* a) {
@@ -292,7 +300,7 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
   int64_t seg_end;
   run.n_win = run.win_lo = 0;
   if (tile < pl.shared) {
-    const int seg = (int)(tile / pl.prefix_tiles);
+    const int seg = (int)pa_div(tile, pl.prefix_tiles);
     run.own = false;
     run.seq = 0;
     run.row0 = seg * PA_ROWS;
@@ -312,7 +320,7 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
     }
     const int b = lo, kts = cum[b + 1] - cum[b];
     const int64_t rem = u - (int64_t)cum[b] * pl.q_blocks;
-    const int qb = (int)(rem / kts);
+    const int qb = (int)pa_div(rem, kts);
     run.own = true;
     run.seq = b;
     run.row0 = (b * p.nq + qb * PA_QB) * CSA2_H;
@@ -428,7 +436,6 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PaSmem& s = *reinterpret_cast<PaSmem*>(smem_raw);
   const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
-  pdl_launch_dependents();
   if (t == 0) {
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -868,6 +875,9 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       done_run();
     }
   }
+  // The merge's blocks start where this block's end; started earlier they only took
+  // registers and issue slots (512 queries: 487 us instead of 461)
+  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   if (s.abort && t == 0) set_status(p.status, ST_TIMEOUT);
@@ -881,8 +891,11 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
 // All heads of a query share the list of partials.  A CTA takes HEADS heads of one
 // query: all 16 where the queries alone fill the GPU (a CTA's look at the plan
 // costs more than a row's sum), else one, its partials dealt to four groups of 128
-// threads (four channels each) whose sums join in a fixed order.
-constexpr int PM_NT = 512;
+// threads (four channels each) whose sums join in a fixed order and whose first
+// partials are loaded while the weights are found (2K-row prefix: 22 -> 18 us with
+// the plan moved before the wait and its divisions to 32 bits; more registers for
+// more of them cost blocks per SM: 7 x 3 queries 32 us with 3, 36 with 6).
+constexpr int PM_NT = 512, PM_AHEAD = 3;
 template <int HEADS>
 __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams p) {
   __shared__ int64_t slot[2 * PA_MAX_GRID];
@@ -893,7 +906,6 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int qi = blockIdx.x / (CSA2_H / HEADS), h0 = blockIdx.x % (CSA2_H / HEADS) * HEADS;
   pdl_launch_dependents();
-  pdl_wait();
   if (t < 2) sums[t] = 0;
   __syncthreads();
   const int b = qi / p.nq, tq = qi - b * p.nq;
@@ -935,6 +947,17 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
                               : pl.shared_slot(seg, c) + row0 % PA_ROWS;
   }
   __syncthreads();
+  pdl_wait();  // for the partials; the lengths prefix_attn_kernel itself has waited for
+  // The first partials of a lone head, on their way while the weights are found
+  const int g = t >> 7, ch = 4 * (t & 127);
+  float4 ahead[PM_AHEAD];
+#pragma unroll
+  for (int k = 0; k < PM_AHEAD; k++) {
+    const int i = g + 4 * k;
+    ahead[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (HEADS == 1 && i < n && slot[i] >= 0)
+      ahead[k] = ld_now_f4(p.part_o + (slot[i] + h0) * CSA2_D + ch);
+  }
   // ---- weights: a warp per head (a NaN sum stays one)
   if (warp < HEADS) {
     float M = -INFINITY;
@@ -963,7 +986,6 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   }
   __syncthreads();
   // ---- the weighted sums
-  const int g = t >> 7, ch = 4 * (t & 127);
   auto store = [&](int h, float4 acc) {
     const float f = inv[h];
     const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc.x * f, acc.y * f);
@@ -971,26 +993,36 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
     *reinterpret_cast<uint2*>(p.out + (int64_t)(row0 + h0 + h) * CSA2_D + ch) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
   };
-  auto add = [&](int h, int i, float4& acc) {
-    const float wt = w[i][h];
-    if (wt == 0.0f) return;
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot[i] + h0 + h) * CSA2_D + ch);
+  auto add_v = [&](float wt, float4 v, float4& acc) {
     acc.x = fmaf(wt, v.x, acc.x);
     acc.y = fmaf(wt, v.y, acc.y);
     acc.z = fmaf(wt, v.z, acc.z);
     acc.w = fmaf(wt, v.w, acc.w);
   };
+  // (a partial of weight zero is loaded and not added: no branch holds up the next
+  // ones' loads)
+  auto add = [&](int h, int i, float4& acc) {
+    const int64_t at = max(slot[i], (int64_t)0) + h0 + h;
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * CSA2_D + ch);
+    if (w[i][h] != 0.0f) add_v(w[i][h], v, acc);
+  };
   if (HEADS > 1) {
-#pragma unroll 2
+#pragma unroll 1
     for (int h = g; h < HEADS; h += 4) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int i = 0; i < n; i++) add(h, i, acc);
       store(h, acc);
     }
   } else {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < PM_AHEAD; k++) {
+      const int i = g + 4 * k;
+      if (i < n && w[i][0] != 0.0f) add_v(w[i][0], ahead[k], acc);
+    }
 #pragma unroll 4
-    for (int i = g; i < n; i += 4) add(0, i, acc);
+    for (int i = g + 4 * PM_AHEAD; i < n; i += 4) add(0, i, acc);
     if (g > 0) acc_s[g - 1][t & 127] = acc;
     __syncthreads();
     if (g == 0) {

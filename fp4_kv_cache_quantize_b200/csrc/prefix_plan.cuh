@@ -27,6 +27,12 @@ constexpr int PA_SEG = 6;
 // What a tile of n rows costs, relative to others.
 __host__ __device__ inline int pa_cost(int n_rows) { return 14 + n_rows / 32; }
 
+// a / b for a >= 0, b > 0: a 64-bit division takes several times a 32-bit one's
+// instructions, and a call's first tiles wait for a handful of them.
+__host__ __device__ inline int64_t pa_div(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct PaPlan {
   int row_blocks;   // blocks of 64 rows over the whole batch
   int prefix_tiles; // key tiles of the shared prefix
@@ -44,15 +50,15 @@ struct PaPlan {
     total = base + own * q_blocks * cost_o;
   }
   __host__ __device__ int64_t tile_at(int i) const {  // first tile of CTA i
-    const int64_t x = total * i / grid;
-    if (x <= base) return (x + cost_p - 1) / cost_p;
-    return shared + (x - base + cost_o - 1) / cost_o;
+    const int64_t x = pa_div(total * i, grid);
+    if (x <= base) return pa_div(x + cost_p - 1, cost_p);
+    return shared + pa_div(x - base + cost_o - 1, cost_o);
   }
   __host__ __device__ int64_t cost_before(int64_t tile) const {
     return tile < shared ? tile * cost_p : base + (tile - shared) * cost_o;
   }
   __host__ __device__ int cta_of(int64_t tile) const {
-    return (int)(((cost_before(tile) + 1) * grid - 1) / total);
+    return (int)pa_div((cost_before(tile) + 1) * grid - 1, total);
   }
   // first row of the partial of CTA c for a shared / an own segment
   __host__ __device__ int64_t shared_slot(int seg, int c) const {
