@@ -182,21 +182,24 @@ __device__ __forceinline__ int ld_now_s32(const void* a) {
 
 // The row map in two steps, so that the page id's latency has a tile's time:
 // the page id of a position (not waited for), then its pool row.  -1: none (a
-// mapping outside the pool is recorded).
-__device__ __forceinline__ int pa_page(const PrefixParams& p, const PaRun& run, int kt, int r) {
-  const int pos = run.first_pos + kt * PA_KEYS + r;
-  if (kt >= run.kt_cache || pos >= run.n_keys) return -1;
+// mapping outside the pool is recorded).  A thread holds its key's part of the run:
+// position pos + 64 kt of sequence seq, if below n_keys and kt below kt_cache.
+struct PaMap {
+  int pos, n_keys, kt_cache, seq;
+};
+__device__ __forceinline__ int pa_page(const PrefixParams& p, const PaMap& m, int kt) {
+  const int pos = m.pos + kt * PA_KEYS;
+  if (kt >= m.kt_cache || pos >= m.n_keys) return -1;
   if (!p.page_table) return 0;
   const int page = pos >> 6;
   if (page >= p.max_pages) return -2;
-  return ld_now_s32(p.page_table + (int64_t)run.seq * p.max_pages + page);
+  return ld_now_s32(p.page_table + (int64_t)m.seq * p.max_pages + page);
 }
-__device__ __forceinline__ int64_t pa_row(const PrefixParams& p, const PaRun& run, int kt, int r,
-                                          int pid) {
-  const int pos = run.first_pos + kt * PA_KEYS + r;
-  if (kt >= run.kt_cache || pos >= run.n_keys) return -1;
+__device__ __forceinline__ int64_t pa_row(const PrefixParams& p, const PaMap& m, int kt, int pid) {
+  const int pos = m.pos + kt * PA_KEYS;
+  if (kt >= m.kt_cache || pos >= m.n_keys) return -1;
   const int64_t row = p.page_table ? (int64_t)pid * 64 + (pos & 63)
-                                   : (int64_t)run.seq * p.seq_stride + pos;
+                                   : (int64_t)m.seq * p.seq_stride + pos;
   if (pid < 0 || row >= p.pool_rows) {
     set_status(p.status, ST_DEVICE_CHECK);
     return -1;
@@ -220,24 +223,24 @@ __device__ __forceinline__ __half2 e4m3x2_as_f16(uint32_t w) {
 constexpr float PA_TILE_SCALE = 128.0f;
 // Eight FP4 codes (one word) times the scale f as fp16.  A code's bits s, eem go
 // to the fp16 sign and to bits 9..11, which reads as 2^-14 of the E2M1 value
-// (subnormal 0.5 included), by shifts and masks of two codes at once: the
-// conversion instruction has a small share of the ALU's rate (with it the
-// kernel spent 86% of its time in that unit).  f = scale * 2^7 <= 57,344 makes
-// the product value * scale * 2^-7: five significant bits above 2^-18, exact.
-// Codes j and j + 4 become neighbours; Q' has the same order and the outputs are
-// stored through pa_channel.
+// (subnormal 0.5 included): by shifts and masks into the upper byte of the fp16,
+// four codes at once, then bytes to halves (the conversion instruction has a small
+// share of the ALU's rate: with it the kernel spent 86% of its time in that unit).
+// f = scale * 2^7 <= 57,344 makes the product value * scale * 2^-7: five significant
+// bits above 2^-18, exact.  Codes come out in the order 0 2 4 6 1 3 5 7; Q' has the
+// same and the outputs are stored through pa_channel.
 __device__ __forceinline__ uint4 pa_fp4x8(uint32_t w, __half2 f) {
-  uint32_t h[4] = {((w << 12) & 0x80008000u) | ((w << 9) & 0x0E000E00u),
-                   ((w << 8) & 0x80008000u) | ((w << 5) & 0x0E000E00u),
-                   ((w << 4) & 0x80008000u) | ((w << 1) & 0x0E000E00u),
-                   (w & 0x80008000u) | ((w >> 3) & 0x0E000E00u)};
+  const uint32_t even = ((w << 4) & 0x80808080u) | ((w << 1) & 0x0E0E0E0Eu);
+  const uint32_t odd = (w & 0x80808080u) | ((w >> 3) & 0x0E0E0E0Eu);
+  uint32_t h[4] = {__byte_perm(even, 0, 0x1404), __byte_perm(even, 0, 0x3424),
+                   __byte_perm(odd, 0, 0x1404), __byte_perm(odd, 0, 0x3424)};
 #pragma unroll
   for (int k = 0; k < 4; k++) h[k] = pa_h2u(__hmul2(*reinterpret_cast<__half2*>(&h[k]), f));
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 // Channel at place c of a tile row (within its group of eight).
 __device__ __forceinline__ int pa_channel(int c) {
-  return (c & ~7) | ((c & 7) >> 1) | ((c & 1) << 2);
+  return (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1);
 }
 // 32 FP4 codes (16 bytes) with their two E4M3 scales (low half of sc) into four
 // 16-byte pieces cc .. cc + 3 of a swizzled row.
@@ -255,10 +258,8 @@ __device__ __forceinline__ uint4 pa_e4m3x8(uint32_t a, uint32_t b) {
   const __half2 two = __half2(__ushort_as_half(0x4000), __ushort_as_half(0x4000));
   uint32_t h[4];
 #pragma unroll
-  for (int k = 0; k < 4; k++) {
-    const uint32_t w = ((a >> (8 * k)) & 0xFFu) | (((b >> (8 * k)) & 0xFFu) << 16);
-    h[k] = pa_h2u(__hmul2(e4m3x2_as_f16(w), two));
-  }
+  for (int k = 0; k < 4; k++)
+    h[k] = pa_h2u(__hmul2(e4m3x2_as_f16((k & 1 ? b : a) >> (k & 2 ? 8 : 0)), two));
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
@@ -392,7 +393,8 @@ __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& r
         }
         uint32_t o4[4];  // the tile's order of channels
 #pragma unroll
-        for (int j = 0; j < 4; j++) o4[j] = pa_h2u(__floats2half2_rn(g[j], g[j + 4]));
+        for (int j = 0; j < 4; j++)
+          o4[j] = pa_h2u(__floats2half2_rn(g[pa_channel(2 * j)], g[pa_channel(2 * j + 1)]));
         *reinterpret_cast<uint4*>(s.q + (lane >> 2) * PA_QKB + pa_sw(h, 2 * (lane & 3) + k)) =
             make_uint4(o4[0], o4[1], o4[2], o4[3]);
       }
@@ -542,7 +544,8 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     for (;;) {
       const PaRun& run = next_run();
       if (!run.valid) break;
-      const int kt_end = run.kt_end, kt_cache = run.kt_cache;
+      const int kt_end = run.kt_end;
+      const PaMap map = {run.first_pos + r, run.n_keys, run.kt_cache, run.seq};
       uint4 v[4], nv[4];       // by block: this tile's codes, the next one's
       uint32_t sc[4], nsc[4];  // the two scales of the same 32 channels
       auto load = [&](int64_t row) {
@@ -560,21 +563,21 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         nv[b] = make_uint4(0u, 0u, 0u, 0u);
         nsc[b] = 0u;
       }
-      int pid = pa_page(p, run, run.kt, r), pid1 = pa_page(p, run, run.kt + 1, r);
-      int64_t row, next = pa_row(p, run, run.kt, r, pid);
+      int pid = pa_page(p, map, run.kt), pid1 = pa_page(p, map, run.kt + 1);
+      int64_t row, next = pa_row(p, map, run.kt, pid);
       load(next);
       int kt = run.kt;
 #pragma unroll 1
-      for (; kt < kt_cache; kt++, i++) {
+      for (; kt < map.kt_cache; kt++, i++) {
         pid = pid1;
-        pid1 = pa_page(p, run, kt + 2, r);
+        pid1 = pa_page(p, map, kt + 2);
         row = next;
 #pragma unroll
         for (int b = 0; b < 4; b++) {
           v[b] = nv[b];
           sc[b] = nsc[b];
         }
-        next = pa_row(p, run, kt + 1, r, pid);
+        next = pa_row(p, map, kt + 1, pid);
         load(next);
         // A key that is not there, or whose values hold a NaN, becomes zeros: the
         // P = 0 of a row that must not see it would turn NaN in the product
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
           p.part_ml[2 * (run.slot + c) + 1] =
               (s.red[0][c] + s.red[1][c]) + (s.red[2][c] + s.red[3][c]);
         }
-#pragma unroll 2
+#pragma unroll
         for (int g = 0; g < 4 * PA_PART / 16; g++) {  // channel block, 16 rows
           const int r0 = PA_PART * part + 16 * (g >> 2);
           if (r0 >= run.n_rows) continue;
