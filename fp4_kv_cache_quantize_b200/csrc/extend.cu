@@ -15,7 +15,15 @@ namespace csa2 {
 constexpr int EX_NT = 256;
 constexpr int EX_LAYERS_PER_CTA = EX_NT / 64;
 constexpr int EX_COMMIT_BATCH = 512;  // sequences whose counters the last CTA advances
-constexpr int EX_FEW = 512;  // tokens up to which each has a CTA of its own
+// Tokens up to which each has CTAs of its own.  Both ways, without window layers:
+// 256 tokens 12 us (tiles: 17), 512 17 (18), 1,024 25 (16); with 20 layers 512 24
+// (26), 1,024 36 (26).  Runs of one or two tokens never fill a tile's places and
+// windows: 1,024 sequences x 20 layers 63 us (tiles: 102).
+constexpr int EX_FEW = 512;
+// CTAs per SM up to which a token's layers are spread (64 sequences x 20 layers 15 us,
+// 512 43; four layers to a CTA always: 16, 65; with 2 a batch of 16 takes 15 instead
+// of 12).
+constexpr int EX_ROOM = 4;
 
 // Tokens [lo, hi) of sequence b; false if the offsets are out of order or do
 // not start at 0.
@@ -120,7 +128,7 @@ __device__ __forceinline__ void extend_arrive(const ExtendParams& p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    const uint32_t n = gridDim.x * gridDim.y;
+    const uint32_t n = gridDim.x * gridDim.y * gridDim.z;
     last = atomicAdd(p.status + CSA2_WS_ARRIVE_WORD, 1u) == n - 1;
     if (last) p.status[CSA2_WS_ARRIVE_WORD] = 0u;
   }
@@ -147,9 +155,9 @@ __device__ __forceinline__ void window_row(const ExtendParams& p, int b, int l, 
                                               (w2[2] & 0xFFFFu) | (w2[3] << 16));
 }
 
-// One CTA per token (few tokens): part 0 packs the entry and projects its key (256 threads:
+// CTAs for one token (few tokens): part 0 packs the entry and projects its key (256 threads:
 // 8 outputs x 16 channels each, partial sums reduced in a fixed order); parts
-// 1.. convert four layers' window entries each (64 threads per layer).
+// 1.. convert the window entries, four layers at a time (64 threads per layer).
 __device__ __forceinline__ void extend_token(const ExtendParams& p) {
   __shared__ float xs[CSA2_D];
   __shared__ float part[32][CSA2_DI + 1];
@@ -223,9 +231,12 @@ __device__ __forceinline__ void extend_token(const ExtendParams& p) {
     return;
   }
 
-  const int l = (blockIdx.y - (p.x ? 1 : 0)) * EX_LAYERS_PER_CTA + (t >> 6);
-  if (l >= p.n_layers || tok < hi - CSA2_W) return;
-  window_row(p, b, l, tok, p.swa_pos[b] + (tok - lo), t & 63);
+  const int z0 = p.x ? 1 : 0, step = (gridDim.y - z0) * EX_LAYERS_PER_CTA;
+  if (tok < hi - CSA2_W) return;
+  const int spos = p.swa_pos[b] + (tok - lo);
+#pragma unroll 4
+  for (int l = (blockIdx.y - z0) * EX_LAYERS_PER_CTA + (t >> 6); l < p.n_layers; l += step)
+    window_row(p, b, l, tok, spos, t & 63);
 }
 
 __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams p) {
@@ -235,28 +246,34 @@ __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams 
   extend_arrive(p);
 }
 
-// ------------------------------------------------- many tokens: tiles of 64
-// One CTA per SM, two groups of eight warps that each walk tiles of 64 tokens.
+// ------------------------------------------------- many tokens: tiles of 32
+// One CTA per SM, four groups of eight warps that each walk tiles of 32 tokens.
 // cp.async brings a tile's raw rows into the swizzled layout that the MMA reads:
-// the key x W of 64 tokens is one tcgen05 product, M = 64, N = 64, K = 512, with
-// one W in shared memory for both groups.  Under it the rows are packed from the
-// same tile, first the pieces (8 channels) in front of the rotated ones, then the
-// rotated ones, all lanes busy whatever their share of a row, in loops short
-// enough to stay in the instruction cache.  Memory would allow 1,440 bytes a
-// token at its rate; what bounds a tile are its dependent phases (rows, packing,
-// turning, keys), which is why two groups take turns on the SM's issue slots.
-// With few tokens the tiles are shorter (32 or 16, the product's other rows
-// idle), so that every SM has some.
-constexpr int ET_GROUPS = 2;
+// the key x W of the tokens is one tcgen05 product, M = 64, N = 64, K = 512, with
+// one W in shared memory for all groups.  (Rows 32.. of the product are whatever
+// lies behind a chunk, the next chunk or W; their sums are not read.)  Under it the
+// rows are packed from the same tile, first the pieces (8 channels) in front of the
+// rotated ones, then the rotated ones, all lanes busy whatever their share of a row,
+// in loops short enough to stay in the instruction cache.
+//
+// What bounds it: memory allows 1,440 bytes a token at its rate, 32K tokens in
+// 7.2 us; they take 31.  20,000 of the 57,000 cycles are issue slots (some 20
+// instructions a value: packing, fp64 rotation), 10,000 the first tiles' way from
+// memory, and the rest the dependent phases of a tile (rows, packing, turning,
+// keys).  Two groups of 64 tokens took 33, tiles of 16 tokens 42, shares of the
+// packing handed out to warps one by one 35.  With few tokens the tiles are
+// shorter (16), so that every SM has some.
+constexpr int ET_GROUPS = 4;
 constexpr int ET_GT = 256;                              // threads of a group
 constexpr int ET_NT = ET_GROUPS * ET_GT;
-constexpr int ET_TOK = 64;                              // most tokens of a tile: the MMA's M
+constexpr int ET_TOK = 32;                              // most tokens of a tile
+constexpr int ET_M = 64;                                // rows of the product
 constexpr int ET_KB = ET_TOK * 128;                     // one 64-channel chunk of the tile
 
 struct EtGroup {
   int64_t row[2][ET_TOK];                    // by tile parity: pool row, -1: not written
   int pos[2][ET_TOK];                        // rotation position
-  int seq_lo[2], seq_hi[2];                  // lowest and highest sequence of each 32 tokens
+  int seq_lo, seq_hi;                        // lowest and highest sequence of the tile
   uint64_t mbar;
 };
 struct EtSmem {
@@ -295,7 +312,7 @@ __device__ __forceinline__ void prefetch_rope(const RopeParams& r, int pos) {
   for (int i = 0; i < r.dims * 4; i += 128) prefetch_l2(a + i);
 }
 
-// The rows and positions of a tile's tokens (threads 0..63 of the group).
+// The rows and positions of a tile's tokens (the group's first warp).
 __device__ __forceinline__ void et_places(const ExtendParams& p, EtGroup& g, int tile, int buf,
                                           int t) {
   const int tok = tile * p.tile + t;
@@ -318,9 +335,9 @@ __device__ __forceinline__ void et_places(const ExtendParams& p, EtGroup& g, int
   g.pos[buf][t] = pos;
   const int a = __reduce_min_sync(0xffffffffu, seq < 0 ? p.batch : seq);
   const int z = __reduce_max_sync(0xffffffffu, seq);
-  if ((t & 31) == 0) {
-    g.seq_lo[t >> 5] = a;
-    g.seq_hi[t >> 5] = z;
+  if (t == 0) {
+    g.seq_lo = a;
+    g.seq_hi = z;
   }
 }
 
@@ -329,8 +346,8 @@ __device__ __forceinline__ void et_places(const ExtendParams& p, EtGroup& g, int
 // the range is [batch, -1]).
 __device__ __forceinline__ void et_check(const ExtendParams& p, EtGroup& g, int tile, int buf,
                                          int warp, int lane) {
-  const int tok0 = tile * p.tile, seq_hi = max(g.seq_hi[0], g.seq_hi[1]);
-  for (int b = min(g.seq_lo[0], g.seq_lo[1]) + warp; b <= seq_hi; b += ET_GT / 32) {
+  const int tok0 = tile * p.tile, seq_hi = g.seq_hi;
+  for (int b = g.seq_lo + warp; b <= seq_hi; b += ET_GT / 32) {
     int lo, hi;
     if (!run_of(p, b, lo, hi) || lo == hi) continue;
     if (!__all_sync(0xffffffffu, run_fits(p, b, hi - lo, lane, 32)))
@@ -344,11 +361,11 @@ __device__ __forceinline__ void et_check(const ExtendParams& p, EtGroup& g, int 
 // different banks, a row's codes are written 32 bytes at a time or more).
 __device__ __forceinline__ void et_plain(const ExtendParams& p, const uint8_t* a, const EtGroup& g,
                                          int buf, int plain, int t) {
-  const int per_row = ET_GT / p.tile, r = t / per_row;
+  const int per_row = ET_GT / p.tile, r = (t >> 2) & (p.tile - 1);
   const int64_t row = g.row[buf][r];
   if (row < 0) return;
 #pragma unroll 2
-  for (int q = t % per_row; q < plain / 2; q += per_row) {
+  for (int q = (t & 3) + t / (4 * p.tile) * 4; q < plain / 2; q += per_row) {
     uint8_t sb;
     const uint2 codes = fp4_encode16(*reinterpret_cast<const uint4*>(a + et_at(r, 2 * q)),
                                      *reinterpret_cast<const uint4*>(a + et_at(r, 2 * q + 1)), &sb);
@@ -404,6 +421,7 @@ __device__ __forceinline__ void et_turn(const ExtendParams& p, const uint8_t* a,
 __device__ __forceinline__ void et_keys(const ExtendParams& p, const EtGroup& g, int buf,
                                         uint32_t tmem, int warp, int lane) {
   const int quad = warp & 3, part = warp >> 2;
+  if (16 * quad >= p.tile) return;
   const int rk = p.rope_idx.table ? p.rope_idx.dims : 0;  // 0, 32 or 64
   const bool halves = rk && p.rope_idx.style == CSA2_ROPE_HALVES;
   // blocks 2 part, 2 part + 1, + 4, + 5: with HALVES of 64 block n pairs with n +
@@ -483,7 +501,7 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
   // neighbouring tiles go to different CTAs: few tiles spread over all SMs
   int tile = blockIdx.x + grp * gridDim.x;
   fetch(tile);
-  if (warp < 2) et_places(p, g, tile, 0, t);
+  if (warp == 0) et_places(p, g, tile, 0, t);
   cp_async_wait_all();
   fence_proxy_async_smem();
   tc_fence_before();
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
       tc_fence_after();
       if (elect_one()) {
         const uint64_t da = sdesc_k128(smem_u32(a)), db = sdesc_mn128(smem_u32(s.w), 65536, 1024);
-        constexpr uint32_t id = idesc_bf16_f32(ET_TOK, CSA2_DI) | (1u << 16);  // W is read MN-major
+        constexpr uint32_t id = idesc_bf16_f32(ET_M, CSA2_DI) | (1u << 16);  // W is read MN-major
 #pragma unroll
         for (uint32_t k = 0; k < 32; k++)
           umma_bf16(tmem, da + (((k >> 2) * ET_KB + 32 * (k & 3)) >> 4), db + ((k * 2048) >> 4), id,
@@ -511,7 +529,7 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
       __syncwarp();
     }
     const bool more = tile + step < n_tiles;
-    if (more && warp < 2) et_places(p, g, tile + step, buf ^ 1, t);
+    if (more && warp == 0) et_places(p, g, tile + step, buf ^ 1, t);
     et_plain(p, a, g, buf, plain, t);
     et_turn(p, a, g, buf, plain, t);
     const bool ok = mbar_wait(&g.mbar, n & 1, nullptr);
@@ -536,20 +554,19 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
   extend_arrive(p);
 }
 
-// The window entries of many tokens: one CTA per 16 of the last 128 tokens of a
-// sequence's run and layer, 64 threads per row.
+// The window entries of many tokens: gridDim.z CTAs share the last 128 tokens of a
+// sequence's run and layer, 16 at a time, 64 threads per row.
 constexpr int EW_TOK = 16;
 __device__ __forceinline__ void extend_window(const ExtendParams& p) {
-  const int t = threadIdx.x, b = blockIdx.x / (CSA2_W / EW_TOK), part = blockIdx.x % (CSA2_W / EW_TOK);
-  const int l = blockIdx.y, ch = t & 63;
+  const int t = threadIdx.x, b = blockIdx.x, l = blockIdx.y, ch = t & 63;
   int lo, hi;
-  if (!run_of(p, b, lo, hi)) return;
-  const int last = hi - part * EW_TOK, first = max(lo, last - EW_TOK);
-  if (last <= lo) return;
+  if (!run_of(p, b, lo, hi) || hi - (int)blockIdx.z * EW_TOK <= lo) return;
   if (!__syncthreads_and(run_fits(p, b, hi - lo, t, EX_NT))) return;
   const int spos0 = p.swa_pos[b];
-  for (int tok = first + (t >> 6); tok < last; tok += EX_NT / 64)
-    window_row(p, b, l, tok, spos0 + (tok - lo), ch);
+  const int end = max(lo, hi - CSA2_W);
+  for (int last = hi - blockIdx.z * EW_TOK; last > end; last -= gridDim.z * EW_TOK)
+    for (int tok = max(end, last - EW_TOK) + (t >> 6); tok < last; tok += EX_NT / 64)
+      window_row(p, b, l, tok, spos0 + (tok - lo), ch);
 }
 
 __global__ void __launch_bounds__(EX_NT) extend_window_kernel(const ExtendParams p) {
@@ -580,16 +597,21 @@ cudaError_t launch_extend(const ExtendParams& params, cudaStream_t st) {
   // the last launch that writes also advances the counters, unless one CTA would
   // be long at it
   const bool in_last = p.batch <= EX_COMMIT_BATCH;
-  if (p.total <= EX_FEW) {
+  const int sms = num_sms();
+  if (p.total <= EX_FEW || p.total / 2 <= p.batch) {
     p.commit = in_last;
-    cfg.gridDim = dim3(p.total, (p.x ? 1 : 0) +
-                                    (p.n_layers + EX_LAYERS_PER_CTA - 1) / EX_LAYERS_PER_CTA);
+    // a token's layers are spread over CTAs as long as those find room
+    const int quads = (p.n_layers + EX_LAYERS_PER_CTA - 1) / EX_LAYERS_PER_CTA;
+    const int room = EX_ROOM * sms / p.total, most = room > 1 ? room : 1;
+    cfg.gridDim = dim3(p.total, (p.x ? 1 : 0) + (quads < most ? quads : most));
     trace_mark("extend", st);
     if ((e = cudaLaunchKernelEx(&cfg, extend_token_kernel, p)) != cudaSuccess) return e;
   } else {
     if (p.n_layers > 0) {
       p.commit = in_last && !p.x;
-      cfg.gridDim = dim3(p.batch * (CSA2_W / EW_TOK), p.n_layers);
+      // as many as a run of twice the average length keeps busy
+      const int mean = (p.total - 1) / p.batch + 1, most = mean < CSA2_W / 2 ? 2 * mean : CSA2_W;
+      cfg.gridDim = dim3(p.batch, p.n_layers, (most + EW_TOK - 1) / EW_TOK);
       trace_mark("extend_window", st);
       if ((e = cudaLaunchKernelEx(&cfg, extend_window_kernel, p)) != cudaSuccess) return e;
     }
@@ -600,7 +622,6 @@ cudaError_t launch_extend(const ExtendParams& params, cudaStream_t st) {
                                     (int)ET_SMEM);
       });
       if (e != cudaSuccess) return e;
-      const int sms = num_sms();
       p.commit = in_last;
       p.tile = 16;
       while (p.tile < ET_TOK && (p.total + p.tile - 1) / p.tile > sms * ET_GROUPS) p.tile *= 2;

@@ -69,25 +69,39 @@ __device__ __forceinline__ uint32_t fp4_encode8(const float (&f)[8], float group
 
 // Encode one 16-channel group (32 bytes of bf16) in one thread: eight code bytes,
 // the scale's bits in *scale_bits.  The same bits as fp4_encode8 with fewer
-// instructions: the magnitudes' maximum on packed 16-bit integers, and x / s as
-// (x r + C) - C, r = 1 / s rounded, C = 1.5 * 2^12, which rounds the product to a
-// multiple of 2^-11.  A quotient that is an E2M1 midpoint T (1/4 .. 5) becomes T
-// exactly (the product is off by 2^-23 of it); any other is at least 2^-8 of T >=
-// 1/4 away from T (x has 8 significant bits and T s at most 7), further than the
-// 2^-12 that the rounding moves it.  Quotients beyond 6 stay beyond it.  The sign
-// comes from x: the sum turns -0 into +0.
+// instructions, by one argument.  What decides is on which side of a midpoint T of
+// the target type a quotient lies, or that it is T.  T and the divisor have so few
+// bits that a quotient which is not T is at least 2^-8 of T away from it, so an
+// approximate product may be snapped to a grid that is coarser than its error,
+// holds every T, and moves nothing by more than 2^-10 of T:
+//  * the scale, amax / 6 to E4M3: T has at most 5 significant bits, 6 T as many as 7,
+//    amax 8.  amax times fp32(1/6) is off by 2^-23 and snapped to 11 bits (tf32).
+//  * the codes, x / s to E2M1, T = 1/4 .. 5: x has 8 bits, T s at most 7.
+//    (x r + C) - C with r = 1 / s to 2^-22 and C = 1.5 * 2^12 is a multiple of 2^-11.
+//    Quotients beyond 6 stay beyond it.  The sign comes from x: the sum turns -0
+//    into +0.
+__device__ __forceinline__ float tf32_rna(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return __uint_as_float(y);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint2 fp4_encode16(const uint4& a, const uint4& b, uint8_t* scale_bits) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
   for (int k = 1; k < 8; k++) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
-  const float t = __fdiv_rn(__uint_as_float(max(m << 16, m & 0xFFFF0000u)), 6.0f);
+  const float t = tf32_rna(__fmul_rn(__uint_as_float(max(m << 16, m & 0xFFFF0000u)), 1.0f / 6.0f));
   const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(sb, __NV_E4M3)));
   *scale_bits = (uint8_t)sb;
   uint32_t out[2] = {0u, 0u};
   if (s != 0.0f) {
-    const float r = __frcp_rn(s), C = 6144.0f;
+    const float r = rcp_approx(s), C = 6144.0f;
 #pragma unroll
     for (int k = 0; k < 8; k++) {
       const float x0 = bf16_lo(w[k]), x1 = bf16_hi(w[k]);

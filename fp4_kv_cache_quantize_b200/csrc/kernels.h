@@ -204,7 +204,7 @@ struct ExtendParams {
   uint8_t* swa;           // [n_layers][batch][128][512] or NULL
   int32_t* swa_pos;
   int32_t* swa_len;
-  int32_t tile;           // tokens per tile of extend_tile_kernel: 16, 32 or 64
+  int32_t tile;           // tokens per tile of extend_tile_kernel: 16 or 32
   int32_t commit;         // this launch's last CTA advances the counters
   uint32_t* status;
 };
