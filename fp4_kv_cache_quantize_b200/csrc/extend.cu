@@ -277,7 +277,7 @@ struct EtGroup {
   uint64_t mbar;
 };
 struct EtSmem {
-  alignas(1024) uint8_t a[ET_GROUPS][8 * ET_KB];  // raw bf16 rows: chunk kb, 64 rows of 128 B, swizzled
+  alignas(1024) uint8_t a[ET_GROUPS][8 * ET_KB];  // raw bf16 rows: chunk kb, 32 rows of 128 B, swizzled
   alignas(1024) uint8_t w[CSA2_D * 128];          // W: 512 rows (K) of 64 outputs, swizzled
   EtGroup g[ET_GROUPS];
   uint32_t tmem_base;
