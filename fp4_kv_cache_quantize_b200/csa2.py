@@ -339,6 +339,24 @@ def _typed(t, dtypes, shape, what):
     return t
 
 
+def _device(*tensors) -> int:
+    """The one device that all of the arguments' tensors live on."""
+    on = {t.get_device() for t in tensors if t is not None}
+    if len(on) > 1:
+        raise ValueError(f"tensors live on different devices: {sorted(on)}")
+    return on.pop()
+
+
+def _stream_on(device: int, ws, stream) -> int:
+    """The stream's handle, where tensors, workspace and stream are all the current
+    device's (the launch goes there, whatever the pointers)."""
+    here = torch.cuda.current_device()
+    there = {device, ws.get_device()} | (set() if stream is None else {stream.device_index})
+    if there != {here}:
+        raise ValueError(f"tensors, workspace or stream of device {sorted(there)}, the current one is {here}")
+    return _stream(stream)
+
+
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _INT = (torch.int32,)
@@ -361,8 +379,9 @@ def csa2_rope_rows(rope: Rope, x, pos, y, ws, inverse: bool = False, stream=None
     rows, heads, ch = _typed(x, _BF16, None, "x").shape
     _typed(y, _BF16, x.shape, "y")
     _typed(pos, _INT, (rows,), "pos")
+    on = _stream_on(_device(rope.table, x, pos, y), ws, stream)
     _check(_rope_rows(C.byref(rope.s), _ptr(x), _ptr(pos), rows, heads, ch, int(bool(inverse)),
-                      _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+                      _ptr(y), _ptr(ws), ws.numel(), on))
 
 
 class CacheExtend:
@@ -396,6 +415,9 @@ class CacheExtend:
             _typed(swa_len, _INT, (kv.batch,), "swa_len")
         self.keep = (kv, x, w_idx, cu_tokens, pos, rope, rope_idx, rope_swa, x_swa, swa, swa_pos,
                      swa_len)
+        self.device = _device(kv.codes, kv.scales, kv.idx_k, kv.n_rows, kv.page_table, x, w_idx, cu_tokens, pos,
+                              x_swa, swa, swa_pos, swa_len,
+                              *(None if r is None else r.table for r in (rope, rope_idx, rope_swa)))
         none = RopeStruct(None, 0, 0, 0)
         ropes = [none if r is None else r.s for r in (rope, rope_idx, rope_swa)]
         self.desc = ExtendDesc(kv.view, total, _ptr(cu_tokens), _ptr(pos), _ptr(x), _ptr(w_idx),
@@ -403,7 +425,8 @@ class CacheExtend:
 
 
 def csa2_cache_extend(ext: CacheExtend, ws, stream=None):
-    _check(_extend(C.byref(ext.desc), _ptr(ws), ws.numel(), _stream(stream)))
+    on = _stream_on(ext.device, ws, stream)
+    _check(_extend(C.byref(ext.desc), _ptr(ws), ws.numel(), on))
 
 
 class PrefixAttn:
@@ -433,6 +456,7 @@ class PrefixAttn:
         _typed(self.out, _BF16, None, "out")
         if sm_scale is None:
             sm_scale = D ** -0.5
+        self.device = _device(kv.codes, kv.scales, kv.n_rows, kv.page_table, q, swa, swa_len, self.out)
         self.desc = PrefixDesc(kv.view, int(prefix_rows), nq, _ptr(q), _ptr(swa), _ptr(swa_len),
                                float(sm_scale), _ptr(self.out))
 
@@ -445,7 +469,8 @@ def csa2_prefix_attn_workspace_size(attn: PrefixAttn) -> int:
 
 
 def csa2_prefix_attn(attn: PrefixAttn, ws, stream=None):
-    _check(_prefix(C.byref(attn.desc), _ptr(ws), ws.numel(), _stream(stream)))
+    on = _stream_on(attn.device, ws, stream)
+    _check(_prefix(C.byref(attn.desc), _ptr(ws), ws.numel(), on))
 
 
 class Trace:

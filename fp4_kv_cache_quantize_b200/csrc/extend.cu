@@ -477,7 +477,6 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
   const int n_tiles = (p.total + p.tile - 1) / p.tile, step = gridDim.x * ET_GROUPS;
   EtGroup& g = s.g[grp];
   uint8_t* const a = s.a[grp];
-  pdl_launch_dependents();
   if (t == 0) {
     mbar_init(&g.mbar, 1);
     fence_mbar_init();
@@ -507,6 +506,7 @@ __global__ void __launch_bounds__(ET_NT, 1) extend_tile_kernel(const ExtendParam
   tc_fence_before();
   __syncthreads();  // W, the tensor memory's base, the first places
   tc_fence_after();
+  pdl_launch_dependents();  // (with the tensor memory in hand: a kernel that waits for this one may want some)
   const uint32_t tmem = s.tmem_base + 64 * grp;
   et_check(p, g, tile, 0, warp, lane);
   const int turned = p.rope.table ? p.rope.dims : 0;  // rotated channels, at the end of a row

@@ -165,3 +165,64 @@ def test_binding_refuses_wrong_dtypes_and_shapes(lib):
         lib.PrefixAttn(Kv, q, 0, swa=torch.zeros(2, 128, 512, dtype=torch.uint8))
     with pytest.raises(ValueError, match="q has dtype"):
         lib.PrefixAttn(Kv, q.float(), 0)
+
+
+class OnDevice:
+    """Looks like a CUDA tensor to the binding; nothing is ever read through it."""
+
+    def __init__(self, device, *shape, dtype=torch.bfloat16):
+        self.device_index, self.shape, self.dtype, self.is_cuda = device, shape, dtype, True
+
+    def get_device(self):
+        return self.device_index
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P16
+
+
+def test_binding_refuses_other_devices(lib, monkeypatch):
+    """Tensors, a workspace or a stream of another device than the current one:
+    the launch would go to the current device with the other one's addresses."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    on = lambda d, *s, **kw: OnDevice(d, *s, **kw)  # noqa: E731
+    table = {d: lib.Rope(on(d, 4, 32, 2, dtype=torch.float32)) for d in (0, 1)}
+    ws = {d: on(d, 256, dtype=torch.uint8) for d in (0, 1)}
+
+    def rope(t=0, x=0, pos=0, y=0, w=0, stream=None):
+        lib.csa2_rope_rows(table[t], on(x, 3, 16, 512), on(pos, 3, dtype=torch.int32), on(y, 3, 16, 512), ws[w],
+                           stream=stream)
+    for kw in (dict(t=1), dict(x=1), dict(pos=1), dict(y=1)):
+        with pytest.raises(ValueError, match="different devices"):
+            rope(**kw)
+
+    class Stream:
+        device_index, cuda_stream = 1, 0
+    for kw in (dict(t=1, x=1, pos=1, y=1, w=1), dict(w=1), dict(stream=Stream)):
+        with pytest.raises(ValueError, match="the current one is 0"):
+            rope(**kw)
+
+    class Kv:
+        batch, view, idx_k, page_table = 2, lib.KVView(), None, None
+        codes, scales, n_rows = on(1, 64, 256), on(1, 64, 32), on(1, 2)
+    with pytest.raises(ValueError, match="different devices"):
+        lib.PrefixAttn(Kv, on(0, 2, 16, 512), 0, out=on(0, 2, 16, 512))
+    attn = lib.PrefixAttn(Kv, on(1, 2, 16, 512), 0, out=on(1, 2, 16, 512))
+    with pytest.raises(ValueError, match="the current one is 0"):
+        lib.csa2_prefix_attn(attn, ws[0])
+    with pytest.raises(ValueError, match="different devices"):
+        lib.CacheExtend(Kv, on(0, 5, 512), on(0, 512, 64))
+    ext = lib.CacheExtend(Kv, on(1, 5, 512), on(1, 512, 64))
+    with pytest.raises(ValueError, match="the current one is 0"):
+        lib.csa2_cache_extend(ext, ws[1])

@@ -257,6 +257,66 @@ def test_extend_packs_every_finite_bf16(lib, orc, dims):
         assert torch.equal(c.d["scales"].cpu()[row], torch.from_numpy(scales))
 
 
+def test_extend_every_group_maximum(lib, orc):
+    """The many tokens' encoder with every positive finite bf16 as a group's maximum:
+    each scale, ties between two of them included."""
+    top = torch.arange(1, 0x7F80, dtype=torch.int32)
+    top = torch.cat([top, top[:32 * 1020 - len(top)]]).to(torch.int16).view(-1, 1)
+    g = torch.Generator().manual_seed(2)
+    part = (torch.rand((len(top), 15), generator=g) * 2 - 1) * top.view(torch.bfloat16).float()
+    x = torch.cat([part.bfloat16(), top.view(torch.bfloat16)], 1).view(-1, D)
+    c = Case(lib, orc, [len(x)], [0], L=0, dims=0, idx_dims=0)
+    c.x = x
+    c.d["x"].copy_(x)
+    c.run()
+    lib.csa2_sync_status(c.ws)
+    codes, scales = orc.quantize_fp4(x.view(torch.int16).numpy().view(np.uint16))
+    row = rows_of(0, 0, len(x), c.stride, c.page_table)
+    assert torch.equal(c.d["codes"].cpu()[row], torch.from_numpy(codes))
+    assert torch.equal(c.d["scales"].cpu()[row], torch.from_numpy(scales))
+
+
+@pytest.mark.parametrize("counts,L", [
+    ([400] + [3] * 199, 2),    # one long run among short ones: its windows by few CTAs
+    ([1] * 300, 20),           # more tokens than CTAs per layer: a token's layers in a loop
+    ([2] * 290 + [1], 5),      # short runs of more than 512 tokens
+    ([1] * 600, 1),            # counters of more sequences than one CTA advances
+])
+def test_extend_spreads_runs_and_layers(lib, orc, counts, L):
+    n0 = [(37 * b) % 190 for b in range(len(counts))]
+    c = Case(lib, orc, counts, n0, L=L, pos="given")
+    c.run()
+    lib.csa2_sync_status(c.ws)
+    c.check()
+
+
+@pytest.mark.parametrize("many", [3, 700])
+def test_extend_behind_4_gib(lib, orc, many):
+    """Rows whose byte offset in the codes passes 32 bits: the same bits as in a
+    small pool."""
+    c = Case(lib, orc, [many, 1], [60, 5], L=0)
+    pages = 17 * (1 << 20) // PAGE + 64  # of 256 code bytes a row: 4.25 GiB
+    d = c.d
+    far = d["page_table"] + (pages - c.pool // PAGE)
+    big = {k: torch.empty((pages * PAGE, d[k].shape[1]), dtype=d[k].dtype, device="cuda")
+           for k in ("codes", "scales", "idx_k")}
+    for k in big:
+        big[k][-c.pool:] = d[k]
+    n_rows = d["n_rows"].clone()
+    kv = lib.KVCache(big["codes"], big["scales"], big["idx_k"], n_rows, max_rows=2000, page_table=far)
+    style = lib.ROPE_PAIRS
+    ext = lib.CacheExtend(kv, d["x"], d["w"], cu_tokens=d["cu"], rope=lib.Rope(d["tab"], style),
+                          rope_idx=lib.Rope(d["tab_idx"], style))
+    lib.csa2_cache_extend(ext, c.ws)
+    lib.csa2_sync_status(c.ws)
+    c.run()
+    lib.csa2_sync_status(c.ws)
+    for k in big:
+        assert torch.equal(big[k][-c.pool:], d[k]), k
+    assert torch.equal(n_rows, d["n_rows"])
+    c.check()
+
+
 def test_extend_nothing(lib, orc):
     """No tokens at all: counters stay, nothing is written."""
     c = Case(lib, orc, [0, 0], [5, 6])
@@ -266,8 +326,7 @@ def test_extend_nothing(lib, orc):
 
 
 def test_extend_far_position_of_a_long_cache(lib, orc):
-    """Rows whose byte offset passes 32 bits are covered by the pool's int64
-    arithmetic; here the position itself is the last of a 1M-row sequence."""
+    """The position is the last of a 1M-row sequence."""
     c = Case(lib, orc, [2], [(1 << 20) - 70], L=1, pos="given", dims=64, idx_dims=64, shuffle_extra=0)
     c.run()
     lib.csa2_sync_status(c.ws)

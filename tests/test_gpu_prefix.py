@@ -204,6 +204,32 @@ def test_counts_out_of_range_are_clamped(lib, orc):
     c.reference().check(out)
 
 
+def test_pool_behind_4_gib(lib, orc):
+    """Rows whose byte offset in the codes passes 32 bits: the same bits as from a
+    small pool."""
+    c = Case(lib, orc, [700, 650], 600, 2, window=[129, 40], seed=9)
+    near = c.run().clone()
+    lib.csa2_sync_status(c.ws)
+    pages = 17 * (1 << 20) // PAGE + 64  # of 256 code bytes a row: 4.25 GiB
+    d = c.d
+    codes = torch.empty((pages * PAGE, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((pages * PAGE, 32), dtype=torch.uint8, device="cuda")
+    codes[-c.pool:], scales[-c.pool:] = d["codes"], d["scales"]
+    kv = lib.KVCache(codes, scales, None, d["n_rows"], max_rows=c.max_rows,
+                     page_table=d["page_table"] + (pages - c.pool // PAGE))
+    far = lib.PrefixAttn(kv, d["q"], c.prefix, swa=d["swa"], swa_len=d["swa_len"], n_query=c.nq)
+    lib.csa2_prefix_attn(far, c.ws)
+    lib.csa2_sync_status(c.ws)
+    assert torch.equal(far.out, near)
+    c.check()
+
+
+def test_the_largest_batch(lib, orc):
+    """As many sequences as a call may have, each of its own length, empty ones among
+    them; one more is refused (on the host)."""
+    Case(lib, orc, [(7 * b) % 40 for b in range(1024)], 5, paged=False, seed=4).check()
+
+
 def test_shared_rows_are_sequence_zeros(lib, orc):
     """Positions below prefix_rows come from sequence 0's pages for everyone."""
     a = Case(lib, orc, [300, 290], 128, 1, seed=11)
