@@ -334,27 +334,33 @@ def _typed(t, dtypes, shape, what):
     """The argument's dtype and shape, as its C entry point will read it."""
     if t.dtype not in dtypes:
         raise ValueError(f"{what} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
     return t
 
 
 def _device(*tensors) -> int:
     """The one device that all of the arguments' tensors live on."""
-    on = {t.get_device() for t in tensors if t is not None}
-    if len(on) > 1:
-        raise ValueError(f"tensors live on different devices: {sorted(on)}")
-    return on.pop()
+    on = None
+    for t in tensors:
+        if t is None:
+            continue
+        if on is None:
+            on = t.get_device()
+        elif t.get_device() != on:
+            raise ValueError(f"tensors live on different devices: {on} and {t.get_device()}")
+    return on
 
 
 def _stream_on(device: int, ws, stream) -> int:
     """The stream's handle, where tensors, workspace and stream are all the current
     device's (the launch goes there, whatever the pointers)."""
     here = torch.cuda.current_device()
-    there = {device, ws.get_device()} | (set() if stream is None else {stream.device_index})
-    if there != {here}:
-        raise ValueError(f"tensors, workspace or stream of device {sorted(there)}, the current one is {here}")
-    return _stream(stream)
+    if device != here or ws.get_device() != here or (stream is not None and stream.device_index != here):
+        raise ValueError(f"tensors of device {device}, workspace of {ws.get_device()}"
+                         + ("" if stream is None else f", stream of {stream.device_index}")
+                         + f": the current one is {here}")
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits
