@@ -229,12 +229,16 @@ struct PrefixParams {
   uint16_t* out;
   float* part_o;    // partials of the shared tiles, then of the own tiles
   float* part_ml;   // (max, sum) per row, laid out alike
+  uint8_t* image;   // the prefix's tiles in fp16, as the products read them (if the plan has them)
+  uint8_t* image_key;  // per key of them: missing (1), holds a NaN (2)
   int32_t grid;     // CTAs that the work is cut for
   uint32_t* status;
 };
 // CTAs to launch, and the workspace for their partials, from host bounds.
 int prefix_grid(const PrefixParams& p, int num_sms);
 size_t prefix_partial_rows(const PrefixParams& p);
+size_t prefix_image_tiles(const PrefixParams& p);  // 0: the plan has none
+constexpr size_t PREFIX_IMAGE = 64 * CSA2_D * 2;   // bytes of one
 cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t st);
 
 // ------------------------------------------------- context-parallel decode

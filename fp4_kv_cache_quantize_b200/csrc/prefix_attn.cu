@@ -54,6 +54,7 @@ constexpr int PA_NT = 32 * (PA_MMA_WARP + 3);
 // waits than they save: 293).
 constexpr int PA_PARTS = 2;
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
+constexpr int PA_COPY = 8 * PA_KB / PA_PARTS / PA_DQ_WARPS;  // a warp's copy of a part of an image
 constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
 constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
 constexpr uint32_t PA_TMEM_COLS = 512;
@@ -174,6 +175,11 @@ __device__ __forceinline__ uint32_t ld_now_u16(const void* a) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t ld_now_u8(const void* a) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
 __device__ __forceinline__ int ld_now_s32(const void* a) {
   int v;
   asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(a));
@@ -242,11 +248,15 @@ __device__ __forceinline__ uint4 pa_fp4x8(uint32_t w, __half2 f) {
 __device__ __forceinline__ int pa_channel(int c) {
   return (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1);
 }
+// Two E4M3 scales (bits 0 and 16) as pa_fp4x8's factors.
+__device__ __forceinline__ __half2 pa_scale(uint32_t sc) {
+  return __hmul2(e4m3x2_as_f16(sc),
+                 __half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+}
 // 32 FP4 codes (16 bytes) with their two E4M3 scales (low half of sc) into four
 // 16-byte pieces cc .. cc + 3 of a swizzled row.
 __device__ __forceinline__ void pa_put_fp4(uint8_t* row, int sw, int cc, uint4 v, uint32_t sc) {
-  const __half2 s2 = __hmul2(e4m3x2_as_f16((sc & 0xFFu) | ((sc & 0xFF00u) << 8)),
-                             __half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+  const __half2 s2 = pa_scale((sc & 0xFFu) | ((sc & 0xFF00u) << 8));
   const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int c = 0; c < 4; c++)
@@ -261,6 +271,14 @@ __device__ __forceinline__ uint4 pa_e4m3x8(uint32_t a, uint32_t b) {
   for (int k = 0; k < 4; k++)
     h[k] = pa_h2u(__hmul2(e4m3x2_as_f16((k & 1 ? b : a) >> (k & 2 ? 8 : 0)), two));
   return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // umma_bf16 with the descriptors as two words: only the low one (the start
@@ -545,6 +563,38 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       const PaRun& run = next_run();
       if (!run.valid) break;
       const int kt_end = run.kt_end;
+      if (pl.images && !run.own) {
+        // the tiles are there: each warp copies an eighth of each part
+        const uint8_t* src = p.image + (int64_t)run.kt * PREFIX_IMAGE + warp * PA_COPY;
+        const uint8_t* key = p.image_key + (int64_t)run.kt * PA_KEYS + r;
+        uint32_t flag = ld_now_u8(key);
+#pragma unroll 1
+        for (int kt = run.kt; kt < kt_end; kt++, i++, src += PREFIX_IMAGE) {
+          const uint32_t now = flag;
+          if (kt + 1 < kt_end) flag = ld_now_u8(key += PA_KEYS);
+#pragma unroll
+          for (int c = 0; c < PA_PARTS; c++) {
+            const bool ok = i < 2 || pa_wait(&s.empty[i & 1][c], ((i >> 1) - 1) & 1, &s.abort);
+            if (c == 0) s.key[i & 1][r][seg] = (uint8_t)now;
+            __syncwarp();
+            if (lane == 0) {
+              if (ok) {
+                mbar_arrive_expect_tx(&s.full[i & 1][c], PA_COPY);
+                bulk_load(s.tile[i & 1] + (c * 8 + warp) * PA_COPY, src + c * 8 * PA_COPY, PA_COPY,
+                          &s.full[i & 1][c]);
+              } else {
+                mbar_arrive(&s.full[i & 1][c]);
+              }
+            }
+          }
+        }
+        // after an expired wait nobody else may look for the last copies
+        if (s.abort)
+          for (uint32_t k = i - min(i, 2u); k < i; k++)
+            for (int c = 0; c < PA_PARTS; c++) mbar_wait(&s.full[k & 1][c], (k >> 1) & 1, nullptr);
+        done_run();
+        continue;
+      }
       const PaMap map = {run.first_pos + r, run.n_keys, run.kt_cache, run.seq};
       uint4 v[4], nv[4];       // by block: this tile's codes, the next one's
       uint32_t sc[4], nsc[4];  // the two scales of the same 32 channels
@@ -890,6 +940,46 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   }
 }
 
+// The images of the prefix's tiles: a CTA per tile, a warp per eight keys, lane (key of
+// four, piece) with eight channels of each 64-channel chunk, so that a warp writes
+// whole 128-byte lines.
+constexpr int PI_NT = 256;
+__global__ void __launch_bounds__(PI_NT) prefix_image_kernel(const PrefixParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, piece = lane & 7, kt = blockIdx.x;
+  pdl_wait();
+  uint8_t* image = p.image + (int64_t)kt * PREFIX_IMAGE;
+  uint32_t w[2][8], sc[2][8];
+  int64_t row[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int r = 8 * warp + 4 * h + (lane >> 3);
+    const PaMap map = {r, p.prefix, (int)gridDim.x, 0};
+    row[h] = pa_row(p, map, kt, pa_page(p, map, kt));
+#pragma unroll
+    for (int kb = 0; kb < 8; kb++) {
+      w[h][kb] = sc[h][kb] = 0u;
+      if (row[h] < 0) continue;
+      w[h][kb] = __ldg(reinterpret_cast<const uint32_t*>(p.codes + row[h] * (CSA2_D / 2)) + 8 * kb + piece);
+      sc[h][kb] = __ldg(reinterpret_cast<const uint32_t*>(p.scales + row[h] * (CSA2_D / 16)) + kb);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int r = 8 * warp + 4 * h + (lane >> 3);
+    bool nan = false;  // of the whole key: every lane has all of its scales
+#pragma unroll
+    for (int kb = 0; kb < 8; kb++) nan |= has_nan(sc[h][kb]);
+    if (piece == 0) p.image_key[kt * PA_KEYS + r] = (uint8_t)(row[h] < 0 ? 1 : (nan ? 2 : 0));
+#pragma unroll
+    for (int kb = 0; kb < 8; kb++) {
+      const uint32_t b = nan ? 0u : (sc[h][kb] >> (8 * (piece >> 1))) & 0xFFu;
+      *reinterpret_cast<uint4*>(image + kb * PA_KB + pa_sw(r, piece)) =
+          pa_fp4x8(nan ? 0u : w[h][kb], pa_scale(b | (b << 16)));
+    }
+  }
+  pdl_launch_dependents();
+}
+
 // out = sum_i w_i O_i / sum_i w_i l_i over a row's partials, w_i = 2^(m_i - max m).
 // All heads of a query share the list of partials.  A CTA takes HEADS heads of one
 // query: all 16 where the queries alone fill the GPU (a CTA's look at the plan
@@ -1057,6 +1147,11 @@ size_t prefix_partial_rows(const PrefixParams& p) {
          ((size_t)p.batch * pl.q_blocks + pl.grid) * pl.own_rows;
 }
 
+size_t prefix_image_tiles(const PrefixParams& p) {
+  const PaPlan pl = pa_plan(p);
+  return pl.images ? pl.prefix_tiles : 0;
+}
+
 cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t st) {
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int&) {
@@ -1068,6 +1163,16 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t st) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  const size_t images = prefix_image_tiles(p);
+  if (images > 0) {
+    cfg.gridDim = dim3((unsigned)images);
+    cfg.blockDim = dim3(PI_NT);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    trace_mark("prefix_image", st);
+    if ((e = cudaLaunchKernelEx(&cfg, prefix_image_kernel, p)) != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(PA_NT);
   cfg.dynamicSmemBytes = PA_SMEM;

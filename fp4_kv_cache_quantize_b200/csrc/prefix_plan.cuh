@@ -24,7 +24,12 @@ constexpr int PA_QB = PA_ROWS / CSA2_H;  // queries per row block
 constexpr int PA_MAX_GRID = 192;
 constexpr int PA_SEG = 6;
 
-// What a tile of n rows costs, relative to others.
+// Row blocks from which the prefix is turned into fp16 tiles once, by a kernel of its
+// own, instead of by every row block again.
+constexpr int PA_IMAGE_BLOCKS = 4;
+
+// What a tile of n rows costs, relative to others; with its image there already.
+constexpr int PA_IMAGE_COST = 11;
 __host__ __device__ inline int pa_cost(int n_rows) { return 14 + n_rows / 32; }
 
 // a / b for a >= 0, b > 0: a 64-bit division takes several times a 32-bit one's
@@ -36,6 +41,7 @@ __host__ __device__ inline int64_t pa_div(int64_t a, int64_t b) {
 struct PaPlan {
   int row_blocks;   // blocks of 64 rows over the whole batch
   int prefix_tiles; // key tiles of the shared prefix
+  bool images;      // their fp16 images are made first
   int q_blocks;     // row blocks per sequence for its own rows
   int own_rows;     // rows of a partial of an own segment
   int win_tiles;    // window tiles per own segment
@@ -80,7 +86,8 @@ __host__ __device__ inline PaPlan pa_plan(const PrefixParams& p) {
   pl.win_tiles =
       p.swa == nullptr ? 0 : (CSA2_W + (p.nq < PA_QB ? p.nq : PA_QB) - 1 + PA_KEYS - 1) / PA_KEYS;
   pl.shared = pl.row_blocks * pl.prefix_tiles;
-  pl.cost_p = pa_cost(rows < PA_ROWS ? rows : PA_ROWS);
+  pl.images = pl.row_blocks >= PA_IMAGE_BLOCKS;
+  pl.cost_p = pl.images ? PA_IMAGE_COST : pa_cost(rows < PA_ROWS ? rows : PA_ROWS);
   pl.cost_o = pa_cost(pl.own_rows);
   pl.base = pl.total = 0;
   pl.grid = p.grid;
