@@ -2,7 +2,8 @@
 // (csa2_prefix_attn).
 //
 // Every query head of the batch meets the shared rows, so a key tile is read
-// and dequantised once for 64 query rows: S^T = K Q'^T (keys on the MMA's M
+// and dequantised once for 64 query rows, or, where there are many blocks of those,
+// once for all of them by a kernel in front: S^T = K Q'^T (keys on the MMA's M
 // axis) and O^T = V^T P^T (channels on it), fp16 operands, fp32 accumulators
 // in tensor memory.  E2M1 x E4M3 products and E4M3 window values are exact in
 // fp16; a query head is scaled by a power of two into fp16's range.
@@ -23,36 +24,37 @@
 
 namespace csa2 {
 
-// What bounds it: at 64 query rows a 64-key tile costs 1,792 cycles of tensor core
-// (32 S^T steps of 32 cycles, 16 O^T steps of 48), about 2,840 of shared memory's
-// data path (the products read K, V, Q' and P, the warps write K and P) and 2,200 issue
-// slots on each scheduler.  They overlap to 3,550 cycles per tile: shared memory's
-// path is busy 2/3 of the time, the schedulers 55%, the tensor core 40%.
-//   128K-row prefix, 64 sequences (1,024 rows): 478 us, 0.58 PFLOP/s
-//   1M-row prefix, 4 sequences (64 rows): 226 us, 1.34 TB/s of cache rows
+// What bounds it.  At 64 query rows a 64-key tile costs 1,792 cycles of tensor core
+// (32 S^T steps of 32 cycles, 16 O^T steps of 48).  Where row blocks turn their own
+// tiles to fp16 it takes 3,300: shared memory's path is busy for 2,840 of them (the
+// products read K, V, Q' and P, the warps write K and P), each scheduler issues for
+// 2,200.  With the images there it takes 2,600: the chain of a tile buffer, which is
+// its copy (1,500 from request to first byte, 2,600 to last), S^T, softmax (1,300 with
+// its waits) and O^T, one after another but for the parts; there are two buffers.
+//   128K-row prefix, 64 sequences (1,024 rows): 385 us, 0.72 PFLOP/s
+//   16K-row prefix, 2 x 256 queries (8,192 rows): 355 us, 0.80 PFLOP/s
+//   1M-row prefix, 4 sequences (64 rows, no images): 229 us, 1.32 TB/s of cache rows
 //   2K-row prefix, 4 sequences: 18 us, the latencies of one tile a CTA (lengths,
 //   plan, page, rows, products, softmax, partial) and of the merge
 //
-// Roles of a CTA: eight warps turn key tiles into fp16, sixteen run the softmax,
-// one thread issues the S^T products and one the O^T products, one warp works out
-// which tiles come next.  Key tiles are 64 keys so that two fit next to the
+// Roles of a CTA: eight warps turn key tiles into fp16 or copy them, sixteen run the
+// softmax, one thread issues the S^T products and one the O^T products, one warp works
+// out which tiles come next.  Key tiles are 64 keys so that two fit next to the
 // queries: while one is multiplied, the next is written.  S^T then is an M = 64
 // product at half the tensor core's rate, but one that shared memory could not
 // feed faster anyway (4 KB of operands in 32 cycles); a single 128-key tile,
-// filled, multiplied and filled again, took twice as long.  Sixteen dequantising
-// and eight softmax warps, with registers moved between them, took 463 us instead
-// of 475 at 1,024 rows but 519 instead of 500 at 512 rows with queries of their own.
+// filled, multiplied and filled again, took twice as long.
 constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 16;
 constexpr int PA_PART = 4 * PA_ROWS / PA_SM_WARPS;  // query rows of a softmax warp
 constexpr int PA_COLS = PA_PART / 4;                // and of a thread
 constexpr int PA_MMA_WARP = PA_DQ_WARPS + PA_SM_WARPS;
 constexpr int PA_NT = 32 * (PA_MMA_WARP + 3);
-// A tile is written, multiplied and freed in parts of 256 channels: S^T begins with
-// the first part, and the first part is filled again while the second is still in
-// the O^T products (a million-row prefix 247 -> 238 us; in one piece the four steps
-// of a tile take 6,500 cycles one after the other.  Four parts cost more fences and
-// waits than they save: 293).
-constexpr int PA_PARTS = 2;
+// A tile is written, multiplied and freed in parts of 128 channels: S^T begins with
+// the first part, and the first part is filled again while the others are still in
+// the O^T products (2 x 256 queries 374 us with two parts, 356 with four).  Warps that
+// turn codes into fp16 finish two parts at once: each costs them a fence and waits
+// (a million rows: one part 247 us, two 238, four of their own 293).
+constexpr int PA_PARTS = 4;
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
 constexpr int PA_COPY = 8 * PA_KB / PA_PARTS / PA_DQ_WARPS;  // a warp's copy of a part of an image
 constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
@@ -279,6 +281,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// The same into the L2 (128K-row prefix x 64 sequences 394 -> 385 us).
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // umma_bf16 with the descriptors as two words: only the low one (the start
@@ -548,16 +555,19 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     const int seg = lane >> 3, r = 8 * warp + (lane & 7), sw = lane & 7, cc = 4 * (seg & 1);
     // before and after the tile's 128-channel block b is written
     auto begin_part = [&](int b) {
-      constexpr int N = 4 / PA_PARTS;
-      if (b % N == 0 && i >= 2)
-        pa_wait(&s.empty[i & 1][b / N], ((i >> 1) - 1) & 1, &s.abort);
+      if (b % 2 == 0 && i >= 2) {
+        pa_wait(&s.empty[i & 1][b], ((i >> 1) - 1) & 1, &s.abort);
+        pa_wait(&s.empty[i & 1][b + 1], ((i >> 1) - 1) & 1, &s.abort);
+      }
     };
     auto end_part = [&](int b) {
-      constexpr int N = 4 / PA_PARTS;
-      if (b % N != N - 1) return;
+      if (b % 2 != 1) return;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.full[i & 1][b / N]);
+      if (lane == 0) {
+        mbar_arrive(&s.full[i & 1][b - 1]);
+        mbar_arrive(&s.full[i & 1][b]);
+      }
     };
     for (;;) {
       const PaRun& run = next_run();
@@ -571,7 +581,10 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
 #pragma unroll 1
         for (int kt = run.kt; kt < kt_end; kt++, i++, src += PREFIX_IMAGE) {
           const uint32_t now = flag;
-          if (kt + 1 < kt_end) flag = ld_now_u8(key += PA_KEYS);
+          if (kt + 1 < kt_end) {
+            flag = ld_now_u8(key += PA_KEYS);
+            if (lane < PA_PARTS) bulk_prefetch(src + PREFIX_IMAGE + lane * 8 * PA_COPY, PA_COPY);
+          }
 #pragma unroll
           for (int c = 0; c < PA_PARTS; c++) {
             const bool ok = i < 2 || pa_wait(&s.empty[i & 1][c], ((i >> 1) - 1) & 1, &s.abort);

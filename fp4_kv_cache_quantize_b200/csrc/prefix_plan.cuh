@@ -24,9 +24,13 @@ constexpr int PA_QB = PA_ROWS / CSA2_H;  // queries per row block
 constexpr int PA_MAX_GRID = 192;
 constexpr int PA_SEG = 6;
 
-// Row blocks from which the prefix is turned into fp16 tiles once, by a kernel of its
-// own, instead of by every row block again.
-constexpr int PA_IMAGE_BLOCKS = 4;
+// Whether the prefix is turned into fp16 tiles once, by a kernel of its own, instead of
+// by every row block again.  A tile of 64 rows costs 2.6 ns (of all SMs' time) less
+// with its image there, an image 13 ns and the kernel 4.5 us: 16 row blocks of 2,048
+// tiles 395 us (without: 449), 2 of 2,048 102 (80), 8 of 128 47 (46), 6 of 79 35 (32).
+__host__ __device__ inline bool pa_images(int row_blocks, int prefix_tiles) {
+  return (int64_t)(row_blocks - 5) * prefix_tiles >= 2048;
+}
 
 // What a tile of n rows costs, relative to others; with its image there already.
 constexpr int PA_IMAGE_COST = 11;
@@ -86,7 +90,7 @@ __host__ __device__ inline PaPlan pa_plan(const PrefixParams& p) {
   pl.win_tiles =
       p.swa == nullptr ? 0 : (CSA2_W + (p.nq < PA_QB ? p.nq : PA_QB) - 1 + PA_KEYS - 1) / PA_KEYS;
   pl.shared = pl.row_blocks * pl.prefix_tiles;
-  pl.images = pl.row_blocks >= PA_IMAGE_BLOCKS;
+  pl.images = pa_images(pl.row_blocks, pl.prefix_tiles);
   pl.cost_p = pl.images ? PA_IMAGE_COST : pa_cost(rows < PA_ROWS ? rows : PA_ROWS);
   pl.cost_o = pa_cost(pl.own_rows);
   pl.base = pl.total = 0;

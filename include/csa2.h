@@ -492,7 +492,7 @@ csa2_status csa2_cache_extend(const csa2_extend_desc *desc, void *ws, size_t ws_
  * Rows that the page table maps outside the pool are skipped and recorded as
  * CSA2_ERR_DEVICE_CHECK, and so is a count outside its range (clamped).
  * Results do not depend on timing: every sum has a fixed order.
- * Two launches; asynchronous on stream.
+ * Two or three launches; asynchronous on stream.
  */
 enum { CSA2_PREFIX_MAX_BATCH = 1024 };
 

@@ -230,6 +230,76 @@ def test_the_largest_batch(lib, orc):
     Case(lib, orc, [(7 * b) % 40 for b in range(1024)], 5, paged=False, seed=4).check()
 
 
+# Many row blocks over a prefix of some length: its fp16 tiles are made first.
+MANY = dict(nq=256, seed=21)
+
+
+@pytest.mark.parametrize("n_rows,prefix,window,paged", [
+    ([1400, 1290], 1100, [383, 200], True),
+    ([1300, 1000], 1088, None, False),
+])
+def test_many_row_blocks(lib, orc, n_rows, prefix, window, paged):
+    Case(lib, orc, n_rows, prefix, paged=paged, window=window, **MANY).check()
+
+
+def test_many_row_blocks_nan_in_masked_places(lib, orc):
+    """A NaN in a prefix row behind a sequence's end reaches only the others' queries
+    that see the row; so does one in a window."""
+    c = Case(lib, orc, [1000, 1300], 1100, **MANY)
+    clean = c.reference()
+    row = c.page_table[0].long()[1050 // PAGE] * PAGE + 1050 % PAGE
+    c.scales[row, 17] = 0x7F
+    c.build()
+    out = c.run().view(2, 256, H, D).float().cpu().double()
+    lib.csa2_sync_status(c.ws)
+    want, tol = clean.out.view(2, 256, H, D), clean.tol.view(2, 256, H, D)
+    sees = 1300 - 255 + torch.arange(256) > 1050
+    assert out[1, sees].isnan().all()
+    out[1, sees] = want[1, sees]
+    assert ((out - want).abs() <= tol + 1e-30).all()
+
+
+def test_many_row_blocks_unmapped_page(lib, orc):
+    """Skipped and reported: as if the page's positions were not there at all."""
+    c = Case(lib, orc, [1400, 1290], 1100, **MANY)
+    c.page_table[0, 5] = -1
+    c.build()
+    out = c.run()
+    with pytest.raises(lib.Csa2Error) as e:
+        lib.csa2_sync_status(c.ws)
+    assert e.value.status == 7
+    c.page_table = torch.cat([c.page_table[:, :5], c.page_table[:, 6:]], 1)
+    c.n_rows, c.prefix = c.n_rows - PAGE, c.prefix - PAGE
+    c.reference().check(out)
+
+
+def test_many_row_blocks_captured(lib, orc):
+    """A replayed graph reads the rows that are there then, on any stream; two graphs
+    with a workspace each do not meet."""
+    cases = [Case(lib, orc, [1400, 1290], 1100, **MANY), Case(lib, orc, [1200, 1300], 1090, nq=300, seed=22)]
+    graphs = []
+    for c in cases:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c.run()
+        graphs.append(g)
+    for c in cases:
+        c.codes = (c.codes.int() * 7 + 3).to(torch.uint8)
+        c.d["codes"].copy_(c.codes)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for c in cases:
+        lib.csa2_sync_status(c.ws)
+        c.reference().check(c.attn.out)
+
+
 def test_shared_rows_are_sequence_zeros(lib, orc):
     """Positions below prefix_rows come from sequence 0's pages for everyone."""
     a = Case(lib, orc, [300, 290], 128, 1, seed=11)
