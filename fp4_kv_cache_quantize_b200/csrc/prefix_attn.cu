@@ -96,7 +96,7 @@ struct PaRun {
   int first_pos;     // position of key 0 of tile 0
   int n_keys;        // positions of the row map end here
   int win_lo, n_win; // first window row of tile own_tiles, rows of the window
-  bool own;
+  bool own, image;   // image: the run's tiles are there in fp16
   bool valid;        // false: no run is left
   int64_t slot;
 };
@@ -322,6 +322,7 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
                                              bool stop) {
   PaRun run;
   run.valid = tile < tile_end && !stop;
+  run.image = pl.images && tile < pl.shared;
   if (!run.valid) return run;
   int64_t seg_end;
   run.n_win = run.win_lo = 0;
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       const PaRun& run = next_run();
       if (!run.valid) break;
       const int kt_end = run.kt_end;
-      if (pl.images && !run.own) {
+      if (run.image) {
         // the tiles are there: each warp copies an eighth of each part
         const uint8_t* src = p.image + (int64_t)run.kt * PREFIX_IMAGE + warp * PA_COPY;
         const uint8_t* key = p.image_key + (int64_t)run.kt * PA_KEYS + r;
@@ -859,33 +860,33 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       }
       done_run();
     }
+  } else if (warp == PA_MMA_WARP + 2) {
+    // ------------------------------------------------------- the planner
+    int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
+    const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
+    for (bool valid = true; valid; n_run++) {
+      PaRun r;
+      do {  // skips what holds empty tiles only
+        r = pa_next_run(p, pl, s.cum, tile, tile_end, s.abort != 0);
+        if (r.valid) tile += r.line;
+      } while (r.valid && r.kt_end <= r.kt);
+      valid = r.valid;
+      const uint32_t k = n_run;
+      if (k >= 2 && !pa_wait(&s.run_empty[k & 1], ((k >> 1) - 1) & 1, &s.abort)) s.abort = 1;
+      valid = __all_sync(0xffffffffu, valid && !s.abort);
+      if (lane == 0) {
+        if (valid) s.run[k & 1] = r;
+        s.run[k & 1].valid = valid;  // (alone: a role may still be at the run before last)
+        mbar_arrive(&s.run_full[k & 1]);
+      }
+    }
   } else {
     // ------------------------------------------------------ the products
     // S^T from one warp, O^T from another: each waits for its own input only (one
     // thread that took them in turn would hold up the other's), and the loops stay
     // small.  A tile's buffers are free again once its O^T step is done, which
     // follows its S^T and its softmax.
-    if (warp == PA_MMA_WARP + 2) {
-      int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
-      const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
-      for (bool valid = true; valid; n_run++) {
-        PaRun r;
-        do {  // skips what holds empty tiles only
-          r = pa_next_run(p, pl, s.cum, tile, tile_end, s.abort != 0);
-          if (r.valid) tile += r.line;
-        } while (r.valid && r.kt_end <= r.kt);
-        valid = r.valid;
-        const uint32_t k = n_run;
-        if (k >= 2 && !pa_wait(&s.run_empty[k & 1], ((k >> 1) - 1) & 1, &s.abort)) s.abort = 1;
-        valid = __all_sync(0xffffffffu, valid && !s.abort);
-        if (lane == 0) {
-          if (valid) s.run[k & 1] = r;
-          s.run[k & 1].valid = valid;  // (alone: a role may still be at the run before last)
-          mbar_arrive(&s.run_full[k & 1]);
-        }
-      }
-    }
-    while (warp <= PA_MMA_WARP + 1) {
+    for (;;) {
       const PaRun& run = next_run();
       if (!run.valid) break;
       const uint32_t begin = i, end = i + (uint32_t)(run.kt_end - run.kt);
