@@ -31,8 +31,9 @@ namespace csa2 {
 // 2,200.  With the images there it takes 2,600: the chain of a tile buffer, which is
 // its copy (1,500 from request to first byte, 2,600 to last), S^T, softmax (1,300 with
 // its waits) and O^T, one after another but for the parts; there are two buffers.
-//   128K-row prefix, 64 sequences (1,024 rows): 385 us, 0.72 PFLOP/s
-//   16K-row prefix, 2 x 256 queries (8,192 rows): 355 us, 0.80 PFLOP/s
+//   128K-row prefix, 64 sequences (1,024 rows): 383 us, 0.72 PFLOP/s; 403 call after
+//   call, when the power limit takes the clock to 1.85 GHz
+//   16K-row prefix, 2 x 256 queries (8,192 rows): 361 us, 0.80 PFLOP/s; 378 likewise
 //   1M-row prefix, 4 sequences (64 rows, no images): 229 us, 1.32 TB/s of cache rows
 //   2K-row prefix, 4 sequences: 18 us, the latencies of one tile a CTA (lengths,
 //   plan, page, rows, products, softmax, partial) and of the merge
@@ -327,16 +328,18 @@ __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan
   int64_t seg_end;
   run.n_win = run.win_lo = 0;
   if (tile < pl.shared) {
-    const int seg = (int)pa_div(tile, pl.prefix_tiles);
+    const int64_t in_band = (int64_t)pl.band * pl.row_blocks;
+    const int band = (int)pa_div(tile, in_band), len = pl.band_tiles(band);
+    const int at = (int)(tile - band * in_band), block = at / len;
     run.own = false;
     run.seq = 0;
-    run.row0 = seg * PA_ROWS;
+    run.row0 = block * PA_ROWS;
     run.n_rows = min(PA_ROWS, p.batch * p.nq * CSA2_H - run.row0);
-    run.kt = (int)(tile - (int64_t)seg * pl.prefix_tiles);
+    run.kt = band * pl.band + at - block * len;
     run.own_tiles = pl.prefix_tiles;
     run.first_pos = 0;
-    run.slot = pl.shared_slot(seg, blockIdx.x);
-    seg_end = (int64_t)(seg + 1) * pl.prefix_tiles;
+    run.slot = pl.shared_slot(band * pl.row_blocks + block, blockIdx.x);
+    seg_end = tile + (block + 1) * len - at;
     run.n_keys = p.prefix;
   } else {
     const int64_t u = tile - pl.shared;
@@ -1003,10 +1006,13 @@ __global__ void __launch_bounds__(PI_NT) prefix_image_kernel(const PrefixParams 
 // the plan moved before the wait and its divisions to 32 bits; more registers for
 // more of them cost blocks per SM: 7 x 3 queries 32 us with 3, 36 with 6).
 constexpr int PM_NT = 512, PM_AHEAD = 3;
+constexpr int PM_PARTS = PA_MAX_GRID + PA_MAX_BANDS + 1;  // partials of a row
+static_assert(PM_PARTS <= PM_NT, "a thread finds each");
 template <int HEADS>
 __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams p) {
-  __shared__ int64_t slot[2 * PA_MAX_GRID];
-  __shared__ float w[2 * PA_MAX_GRID][HEADS];
+  __shared__ int64_t slot[PM_PARTS];
+  __shared__ float w[PM_PARTS][HEADS];
+  __shared__ int seg_first[PA_MAX_BANDS + 1], seg_end[PA_MAX_BANDS + 1];
   __shared__ int sums[2];
   __shared__ float inv[HEADS];
   __shared__ float4 acc_s[3][128];
@@ -1033,25 +1039,36 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   pl.finish(sums[0]);
   const int kts = pa_own_line(p, pl, p.n_rows[b]);
 
-  // ---- the query's partials (row of head 0): shared segment, then own segment
-  const int qb = tq / PA_QB, row0 = qi * CSA2_H, seg = row0 / PA_ROWS, oseg = b * pl.q_blocks + qb;
-  const int64_t ts[2] = {(int64_t)seg * pl.prefix_tiles,
-                         pl.shared + (int64_t)sums[1] * pl.q_blocks + (int64_t)qb * kts};
-  const int64_t te[2] = {ts[0] + pl.prefix_tiles, ts[1] + kts};
-  int first[2] = {0, 0}, count[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; k++) {
-    if (te[k] > ts[k]) {
-      first[k] = pl.cta_of(ts[k]);
-      count[k] = pl.cta_of(te[k] - 1) - first[k] + 1;
-    }
+  // ---- the query's partials (row of head 0): its shared segments', then its own's;
+  // at most one for each CTA and one more for each segment
+  const int qb = tq / PA_QB, row0 = qi * CSA2_H, block = row0 / PA_ROWS, oseg = b * pl.q_blocks + qb;
+  auto tiles_of = [&](int k, int64_t& ts, int64_t& te) {  // of band k, or k = bands: own
+    ts = k < pl.bands ? pl.shared_tile(k, block)
+                      : pl.shared + (int64_t)sums[1] * pl.q_blocks + (int64_t)qb * kts;
+    te = ts + (k < pl.bands ? (pl.prefix_tiles > 0 ? pl.band_tiles(k) : 0) : kts);
+  };
+  if (t <= pl.bands) {
+    int64_t ts, te;
+    tiles_of(t, ts, te);
+    seg_first[t] = te > ts ? pl.cta_of(ts) : 0;
+    seg_end[t] = te > ts ? pl.cta_of(te - 1) - seg_first[t] + 1 : 0;  // (its count)
   }
-  const int n = count[0] + count[1];
-  if (t < n) {  // n <= 2 * PA_MAX_GRID <= PM_NT
-    const int k = t < count[0] ? 0 : 1, c = first[k] + (k ? t - count[0] : t);
-    const int64_t a = max(pl.tile_at(c), ts[k] + (k ? PA_SEG : 0)), z = min(pl.tile_at(c + 1), te[k]);
-    slot[t] = a >= z ? -1 : k ? pl.own_slot(oseg, c) + (tq - qb * PA_QB) * CSA2_H
-                              : pl.shared_slot(seg, c) + row0 % PA_ROWS;
+  __syncthreads();
+  if (t == 0)
+    for (int k = 1; k <= pl.bands; k++) seg_end[k] += seg_end[k - 1];
+  __syncthreads();
+  const int n = seg_end[pl.bands];
+  if (t < n) {
+    int k = 0;
+    while (t >= seg_end[k]) k++;
+    const int c = seg_first[k] + t - (k > 0 ? seg_end[k - 1] : 0);
+    const bool own = k == pl.bands;
+    int64_t ts, te;
+    tiles_of(k, ts, te);
+    const int64_t from = max(pl.tile_at(c), ts + (own ? PA_SEG : 0)), to = min(pl.tile_at(c + 1), te);
+    slot[t] = from >= to ? -1
+              : own      ? pl.own_slot(oseg, c) + (tq - qb * PA_QB) * CSA2_H
+                         : pl.shared_slot(k * pl.row_blocks + block, c) + row0 % PA_ROWS;
   }
   __syncthreads();
   pdl_wait();  // for the partials; the lengths prefix_attn_kernel itself has waited for
@@ -1157,7 +1174,7 @@ int prefix_grid(const PrefixParams& p, int num_sms) {
 
 size_t prefix_partial_rows(const PrefixParams& p) {
   const PaPlan pl = pa_plan(p);
-  return (size_t)(pl.row_blocks + pl.grid) * PA_ROWS +
+  return (size_t)(pl.row_blocks * pl.bands + pl.grid) * PA_ROWS +
          ((size_t)p.batch * pl.q_blocks + pl.grid) * pl.own_rows;
 }
 

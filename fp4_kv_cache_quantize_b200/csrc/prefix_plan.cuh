@@ -2,9 +2,9 @@
 // for the kernel that computes the partials and the one that merges them.
 //
 // A tile is 64 keys against up to 64 query rows (a row is one head of one
-// query).  A segment is every key tile of one row block: first the blocks of 64
-// rows of the whole batch against the shared prefix, then, per sequence, its
-// blocks of up to four queries against its own rows and its window.  The tiles
+// query).  A segment is the key tiles of one row block: first the blocks of 64
+// rows of the whole batch against the shared prefix, band by band of it, then, per
+// sequence, its blocks of up to four queries against its own rows and its window.  The tiles
 // lie on one line in segment order, each as long as it costs, and CTA i of G
 // takes the tiles that start in [i C / G, (i + 1) C / G): every CTA gets an
 // equal share whatever the lengths, and one partial per segment that it touches.
@@ -32,6 +32,19 @@ __host__ __device__ inline bool pa_images(int row_blocks, int prefix_tiles) {
   return (int64_t)(row_blocks - 5) * prefix_tiles >= 2048;
 }
 
+// Bands of the prefix: one, but with images several, so that CTAs which run at the
+// same time read the same ones while they are in the L2: about as long as a CTA's
+// share, and at most 512 tiles (32 MB), as far as PA_MAX_BANDS go.  In one band the
+// row blocks meet an image a whole prefix apart, and 134 MB of them (128K rows) came
+// from memory four times: 64 sequences took as long while the GPU was cool, but 440
+// us instead of 403 call after call, at its power limit.
+constexpr int PA_MAX_BANDS = 16;
+__host__ __device__ inline int pa_bands(bool images, int row_blocks, int prefix_tiles, int grid) {
+  if (!images) return 1;
+  const int a = grid / row_blocks, b = (prefix_tiles + 511) / 512, n = a > b ? a : b;
+  return n < 1 ? 1 : n < PA_MAX_BANDS ? n : PA_MAX_BANDS;
+}
+
 // What a tile of n rows costs, relative to others; with its image there already.
 constexpr int PA_IMAGE_COST = 11;
 __host__ __device__ inline int pa_cost(int n_rows) { return 14 + n_rows / 32; }
@@ -46,6 +59,7 @@ struct PaPlan {
   int row_blocks;   // blocks of 64 rows over the whole batch
   int prefix_tiles; // key tiles of the shared prefix
   bool images;      // their fp16 images are made first
+  int band, bands;  // tiles of a band (the last may have fewer), bands
   int q_blocks;     // row blocks per sequence for its own rows
   int own_rows;     // rows of a partial of an own segment
   int win_tiles;    // window tiles per own segment
@@ -70,12 +84,19 @@ struct PaPlan {
   __host__ __device__ int cta_of(int64_t tile) const {
     return (int)pa_div((cost_before(tile) + 1) * grid - 1, total);
   }
+  // segment k row_blocks + b is row block b's of band k
+  __host__ __device__ int band_tiles(int k) const {
+    return prefix_tiles - k * band < band ? prefix_tiles - k * band : band;
+  }
+  __host__ __device__ int64_t shared_tile(int k, int b) const {  // its first on the line
+    return (int64_t)k * band * row_blocks + (int64_t)b * band_tiles(k);
+  }
   // first row of the partial of CTA c for a shared / an own segment
   __host__ __device__ int64_t shared_slot(int seg, int c) const {
     return (int64_t)(seg + c) * PA_ROWS;
   }
   __host__ __device__ int64_t own_slot(int seg, int c) const {
-    return (int64_t)(row_blocks + grid) * PA_ROWS + (int64_t)(seg + c) * own_rows;
+    return (int64_t)(row_blocks * bands + grid) * PA_ROWS + (int64_t)(seg + c) * own_rows;
   }
 };
 
@@ -91,6 +112,9 @@ __host__ __device__ inline PaPlan pa_plan(const PrefixParams& p) {
       p.swa == nullptr ? 0 : (CSA2_W + (p.nq < PA_QB ? p.nq : PA_QB) - 1 + PA_KEYS - 1) / PA_KEYS;
   pl.shared = pl.row_blocks * pl.prefix_tiles;
   pl.images = pa_images(pl.row_blocks, pl.prefix_tiles);
+  pl.bands = pa_bands(pl.images, pl.row_blocks, pl.prefix_tiles, p.grid);
+  pl.band = (pl.prefix_tiles + pl.bands - 1) / pl.bands;
+  if (pl.band > 0) pl.bands = (pl.prefix_tiles + pl.band - 1) / pl.band;
   pl.cost_p = pl.images ? PA_IMAGE_COST : pa_cost(rows < PA_ROWS ? rows : PA_ROWS);
   pl.cost_o = pa_cost(pl.own_rows);
   pl.base = pl.total = 0;

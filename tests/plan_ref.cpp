@@ -41,7 +41,7 @@ extern "C" int plan_check(int batch, int nq, int prefix, int max_rows, const int
   }
   *mean_cost = pl.total / grid;
   // slots: workspace rows as prefix_partial_rows counts them
-  const int64_t rows = (int64_t)(pl.row_blocks + grid) * PA_ROWS +
+  const int64_t rows = (int64_t)(pl.row_blocks * pl.bands + grid) * PA_ROWS +
                        ((int64_t)batch * pl.q_blocks + grid) * pl.own_rows;
   std::set<std::pair<int64_t, int64_t>> taken;
   auto segment = [&](int64_t ts, int64_t te, int seg, bool own) {
@@ -60,9 +60,17 @@ extern "C" int plan_check(int batch, int nq, int prefix, int max_rows, const int
     }
     return 0;
   };
-  for (int i = 0; i < pl.row_blocks; i++)
-    if (int e = segment((int64_t)i * pl.prefix_tiles, (int64_t)(i + 1) * pl.prefix_tiles, i, false))
-      return e;
+  int64_t next = 0;
+  if (pl.bands < 1 || pl.bands > PA_MAX_BANDS) return 9;
+  if (pl.prefix_tiles > 0)
+    for (int k = 0; k < pl.bands; k++)
+      for (int i = 0; i < pl.row_blocks; i++) {
+        const int64_t ts = pl.shared_tile(k, i), te = ts + pl.band_tiles(k);
+        if (ts != next || te <= ts) return 10;
+        next = te;
+        if (int e = segment(ts, te, k * pl.row_blocks + i, false)) return e;
+      }
+  if (next != pl.shared) return 11;
   for (int b = 0; b < batch; b++) {
     const int kts = cum[b + 1] - cum[b];
     for (int qb = 0; qb < pl.q_blocks; qb++) {
