@@ -507,7 +507,9 @@ typedef struct {
   uint16_t *out;
 } csa2_prefix_desc;
 
-/* Workspace bytes of csa2_prefix_attn; 0 on a bad argument. */
+/* Workspace bytes of csa2_prefix_attn; 0 on a bad argument.  Partial results,
+ * and, where many queries share a long prefix, its rows in fp16 (1,025 bytes a
+ * row), made anew by every call. */
 size_t csa2_prefix_attn_workspace_size(const csa2_prefix_desc *desc);
 csa2_status csa2_prefix_attn(const csa2_prefix_desc *desc, void *ws, size_t ws_bytes,
                              csa2_stream_t stream);
