@@ -112,8 +112,8 @@ csa2_status csa2_rope_rows(const csa2_rope* rope, const uint16_t* x, const int32
   CSA2_REQUIRE(rope != nullptr, CSA2_ERR_INVALID_ARG, "rope is NULL");
   CSA2_REQUIRE(ch > 0 && ch % 8 == 0 && ch <= 65536, CSA2_ERR_SHAPE,
                "ch = %d is not a multiple of 8 up to 65536", ch);
-  CSA2_REQUIRE(rows >= 0 && heads >= 0, CSA2_ERR_SHAPE, "rows = %lld, heads = %d",
-               (long long)rows, heads);
+  CSA2_REQUIRE(rows >= 0 && heads >= 0 && heads <= 65536, CSA2_ERR_SHAPE,
+               "rows = %lld, heads = %d (up to 65536)", (long long)rows, heads);
   CSA2_REQUIRE_PTR(rope->table);
   csa2_status r = check_rope(*rope, "rope", ch);
   if (r) return r;

@@ -396,7 +396,8 @@ typedef struct {
  *   x, y   bf16 [rows][heads][ch]; y == x rotates in place (then only the
  *          rotated channels are touched); otherwise they must not overlap.
  *   pos    int32 [rows], 4-byte aligned;  ch a multiple of 8, ch <= 65536;
- *          rows, heads >= 0 with rows * heads * ch < 2^40; 0 rows do nothing.
+ *          rows >= 0 and heads in [0, 65536] with rows * heads * ch < 2^40; 0 rows do
+ *          nothing.
  *   ws     a workspace of at least CSA2_WS_HEADER bytes (status word).
  */
 csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32_t *pos,

@@ -167,6 +167,10 @@ def test_binding_refuses_wrong_dtypes_and_shapes(lib):
         lib.PrefixAttn(Kv, q.float(), 0)
 
 
+def test_rope_refuses_too_many_heads(lib):
+    assert rope_call(lib, rows=1, heads=65537, ch=64, r=rope(lib, dims=32)) == SHAPE
+
+
 class OnDevice:
     """Looks like a CUDA tensor to the binding; nothing is ever read through it."""
 
