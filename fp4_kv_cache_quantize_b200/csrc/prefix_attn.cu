@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int before = incl - sum;
-    for (int w = 0; w < warp; w++) before += s.wsum[w];
+    static_assert(PA_NT <= 32 * 32, "a lane per warp");
+    int before = incl - sum + (int)__reduce_add_sync(0xffffffffu, lane < warp ? s.wsum[lane] : 0);
 #pragma unroll
     for (int k = 0; k < PER; k++) {
       const int b = PER * t + k;
@@ -865,8 +865,9 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
     }
   } else if (warp == PA_MMA_WARP + 2) {
     // ------------------------------------------------------- the planner
-    int64_t tile = pl.total > 0 ? pl.tile_at(blockIdx.x) : 0;
-    const int64_t tile_end = pl.total > 0 ? pl.tile_at(blockIdx.x + 1) : 0;
+    const int64_t share = pl.total > 0 ? pl.tile_at(blockIdx.x + (lane & 1)) : 0;
+    int64_t tile = __shfl_sync(0xffffffffu, share, 0);
+    const int64_t tile_end = __shfl_sync(0xffffffffu, share, 1);
     for (bool valid = true; valid; n_run++) {
       PaRun r;
       do {  // skips what holds empty tiles only
