@@ -22,7 +22,7 @@ constexpr int PA_KEYS = 64;      // keys per tile: the MMA's M
 constexpr int PA_ROWS = 64;      // query rows per tile: the MMA's N
 constexpr int PA_QB = PA_ROWS / CSA2_H;  // queries per row block
 constexpr int PA_MAX_GRID = 192;
-constexpr int PA_SEG = 6;
+constexpr int PA_SEG = 6;  // (2 x 256 queries: 544 us with 4, 498 with 6; 64 x 1 477 and 479)
 
 // Whether the prefix is turned into fp16 tiles once, by a kernel of its own, instead of
 // by every row block again.  A tile of 64 rows costs 2.6 ns (of all SMs' time) less
@@ -45,7 +45,8 @@ __host__ __device__ inline int pa_bands(bool images, int row_blocks, int prefix_
   return n < 1 ? 1 : n < PA_MAX_BANDS ? n : PA_MAX_BANDS;
 }
 
-// What a tile of n rows costs, relative to others; with its image there already.
+// What a tile of n rows costs, relative to others; with its image there already (64 x
+// 1 and 2 x 256 queries: 428 and 372 us with 8, 396 and 358 with 11, 390 and 393 with 13).
 constexpr int PA_IMAGE_COST = 11;
 __host__ __device__ inline int pa_cost(int n_rows) { return 14 + n_rows / 32; }
 
