@@ -57,7 +57,7 @@ constexpr int PA_NT = 32 * (PA_MMA_WARP + 3);
 // (a million rows: one part 247 us, two 238, four of their own 293).
 constexpr int PA_PARTS = 4;
 constexpr int PA_KB = PA_KEYS * 128;   // one 64-channel chunk of a key tile
-constexpr int PA_COPY = 8 * PA_KB / PA_PARTS / PA_DQ_WARPS;  // a warp's copy of a part of an image
+constexpr int PA_COPY = 8 * PA_KB / PA_PARTS;  // a part of an image
 constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
 constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
 constexpr uint32_t PA_TMEM_COLS = 512;
@@ -152,6 +152,10 @@ __device__ __forceinline__ bool bar_or_128(int id, bool v) {
       : "r"((uint32_t)v), "r"(id)
       : "memory");
   return r != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
 // Loads that stay where they are written: a plain read-only load may be moved
@@ -533,7 +537,8 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
   // part of this one is done (the tiles' barriers keep it from running away).
   // Tile i of the CTA uses buffers i & 1; their barriers' phase is (i >> 1) & 1.
   // Named barriers 1 to 4: the softmax warps of 16 rows, 5: all softmax warps,
-  // BAR_Q: a run's queries are in shared memory (softmax and MMA warps).
+  // BAR_Q: a run's queries are in shared memory (softmax and MMA warps), 7: an image
+  // run is on its way (the warps that fill tiles).
   constexpr int BAR_Q = 6, Q_THREADS = 32 * (PA_SM_WARPS + 2);
   uint32_t n_run = 0;
   // Waits for the next run's plan.  The planner always gives one (after an expired
@@ -578,37 +583,49 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
       if (!run.valid) break;
       const int kt_end = run.kt_end;
       if (run.image) {
-        // the tiles are there: each warp copies an eighth of each part
-        const uint8_t* src = p.image + (int64_t)run.kt * PREFIX_IMAGE + warp * PA_COPY;
-        const uint8_t* key = p.image_key + (int64_t)run.kt * PA_KEYS + r;
-        uint32_t flag = ld_now_u8(key);
+        // the tiles are there: one warp copies them for all eight
+        if (warp == 0) {
+          const uint8_t* src = p.image + (int64_t)run.kt * PREFIX_IMAGE;
+          const uint8_t* key = p.image_key + (int64_t)run.kt * PA_KEYS + lane;
+          uint32_t flag0 = ld_now_u8(key), flag1 = ld_now_u8(key + 32);
 #pragma unroll 1
-        for (int kt = run.kt; kt < kt_end; kt++, i++, src += PREFIX_IMAGE) {
-          const uint32_t now = flag;
-          if (kt + 1 < kt_end) {
-            flag = ld_now_u8(key += PA_KEYS);
-            if (lane < PA_PARTS) bulk_prefetch(src + PREFIX_IMAGE + lane * 8 * PA_COPY, PA_COPY);
-          }
+          for (int kt = run.kt; kt < kt_end; kt++, i++, src += PREFIX_IMAGE) {
+            const uint32_t now0 = flag0, now1 = flag1;
+            if (kt + 1 < kt_end) {
+              key += PA_KEYS;
+              flag0 = ld_now_u8(key);
+              flag1 = ld_now_u8(key + 32);
+              if (lane < PA_PARTS) bulk_prefetch(src + PREFIX_IMAGE + lane * PA_COPY, PA_COPY);
+            }
 #pragma unroll
-          for (int c = 0; c < PA_PARTS; c++) {
-            const bool ok = i < 2 || pa_wait(&s.empty[i & 1][c], ((i >> 1) - 1) & 1, &s.abort);
-            if (c == 0) s.key[i & 1][r][seg] = (uint8_t)now;
-            __syncwarp();
-            if (lane == 0) {
-              if (ok) {
-                mbar_arrive_expect_tx(&s.full[i & 1][c], PA_COPY);
-                bulk_load(s.tile[i & 1] + (c * 8 + warp) * PA_COPY, src + c * 8 * PA_COPY, PA_COPY,
-                          &s.full[i & 1][c]);
-              } else {
-                mbar_arrive(&s.full[i & 1][c]);
+            for (int c = 0; c < PA_PARTS; c++) {
+              const bool ok = i < 2 || pa_wait(&s.empty[i & 1][c], ((i >> 1) - 1) & 1, &s.abort);
+              if (c == 0) {
+                *reinterpret_cast<uint32_t*>(s.key[i & 1][lane]) = now0;
+                *reinterpret_cast<uint32_t*>(s.key[i & 1][lane + 32]) = now1;
+              }
+              __syncwarp();
+              if (lane == 0) {
+                if (ok) {
+                  mbar_arrive_expect_tx(&s.full[i & 1][c], PA_COPY);
+                  bulk_load(s.tile[i & 1] + c * PA_COPY, src + c * PA_COPY, PA_COPY,
+                            &s.full[i & 1][c]);
+                } else {
+                  mbar_arrive(&s.full[i & 1][c]);
+                }
+                mbar_arrive_n(&s.full[i & 1][c], PA_DQ_WARPS - 1);
               }
             }
           }
+          // after an expired wait nobody else may look for the last copies
+          if (s.abort)
+            for (uint32_t k = i - min(i, 2u); k < i; k++)
+              for (int c = 0; c < PA_PARTS; c++) mbar_wait(&s.full[k & 1][c], (k >> 1) & 1, nullptr);
+        } else {
+          i += (uint32_t)(kt_end - run.kt);
         }
-        // after an expired wait nobody else may look for the last copies
-        if (s.abort)
-          for (uint32_t k = i - min(i, 2u); k < i; k++)
-            for (int c = 0; c < PA_PARTS; c++) mbar_wait(&s.full[k & 1][c], (k >> 1) & 1, nullptr);
+        // the others' next waits are for phases that come after this run's
+        bar_sync<32 * PA_DQ_WARPS>(7);
         done_run();
         continue;
       }
