@@ -31,15 +31,15 @@ namespace csa2 {
 // 2,200.  With the images there it takes 2,600: the chain of a tile buffer, which is
 // its copy (1,500 from request to first byte, 2,600 to last), S^T, softmax (1,300 with
 // its waits) and O^T, one after another but for the parts; there are two buffers.
-//   128K-row prefix, 64 sequences (1,024 rows): 383 us, 0.72 PFLOP/s; 403 call after
+//   128K-row prefix, 64 sequences (1,024 rows): 376 us, 0.74 PFLOP/s; 389 call after
 //   call, when the power limit takes the clock to 1.85 GHz
-//   16K-row prefix, 2 x 256 queries (8,192 rows): 361 us, 0.80 PFLOP/s; 378 likewise
-//   1M-row prefix, 4 sequences (64 rows, no images): 229 us, 1.32 TB/s of cache rows
-//   2K-row prefix, 4 sequences: 18 us, the latencies of one tile a CTA (lengths,
+//   16K-row prefix, 2 x 256 queries (8,192 rows): 367 us, 0.79 PFLOP/s; 369 likewise
+//   1M-row prefix, 4 sequences (64 rows, no images): 227 us, 1.27 TB/s of cache rows
+//   2K-row prefix, 4 sequences: 17 us, the latencies of one tile a CTA (lengths,
 //   plan, page, rows, products, softmax, partial) and of the merge
 //
-// Roles of a CTA: eight warps turn key tiles into fp16 or copy them, sixteen run the
-// softmax, one thread issues the S^T products and one the O^T products, one warp works
+// Roles of a CTA: eight warps turn key tiles into fp16 (or one of them copies images:
+// all eight took 402 us instead of 389, in power), sixteen run the softmax, one thread issues the S^T products and one the O^T products, one warp works
 // out which tiles come next.  Key tiles are 64 keys so that two fit next to the
 // queries: while one is multiplied, the next is written.  S^T then is an M = 64
 // product at half the tensor core's rate, but one that shared memory could not
@@ -288,7 +288,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// The same into the L2 (128K-row prefix x 64 sequences 394 -> 385 us).
+// The same into the L2, one tile ahead (128K-row prefix x 64 sequences 394 -> 385 us).
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
