@@ -39,10 +39,11 @@ namespace csa2 {
 //   plan, page, rows, products, softmax, partial) and of the merge
 //
 // Roles of a CTA: eight warps turn key tiles into fp16 (or one of them copies images:
-// all eight took 402 us instead of 389, in power), sixteen run the softmax, one thread issues the S^T products and one the O^T products, one warp works
-// out which tiles come next.  Key tiles are 64 keys so that two fit next to the
-// queries: while one is multiplied, the next is written.  S^T then is an M = 64
-// product at half the tensor core's rate, but one that shared memory could not
+// all eight took 402 us instead of 389, in power), sixteen run the softmax, one thread
+// issues the S^T products and one the O^T products, one warp works out which tiles
+// come next.  Key tiles are 64 keys so that two fit next to the queries: while one is
+// multiplied, the next is written.  S^T then is an M = 64 product at half the tensor
+// core's rate, but one that shared memory could not
 // feed faster anyway (4 KB of operands in 32 cycles); a single 128-key tile,
 // filled, multiplied and filled again, took twice as long.
 constexpr int PA_DQ_WARPS = 8, PA_SM_WARPS = 16;
