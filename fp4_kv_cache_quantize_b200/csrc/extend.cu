@@ -7,6 +7,7 @@
 // a whole, so every CTA that writes for a sequence first checks the sequence's
 // whole run; what advances the counters makes the same check.
 #include "csa2_internal.cuh"
+#include "extend_runs.cuh"
 #include "umma_m64.cuh"
 #include "rope.cuh"
 
@@ -25,28 +26,8 @@ constexpr int EX_FEW = 512;
 // of 12).
 constexpr int EX_ROOM = 4;
 
-// Tokens [lo, hi) of sequence b; false if the offsets are out of order or do
-// not start at 0.
-__device__ __forceinline__ bool run_of(const ExtendParams& p, int b, int& lo, int& hi) {
-  if (!p.cu) {
-    lo = b;
-    hi = b + 1;
-    return true;
-  }
-  lo = __ldg(p.cu + b);
-  hi = __ldg(p.cu + b + 1);
-  return lo >= 0 && hi >= lo && hi <= p.total && (b > 0 || lo == 0);
-}
-
-// The sequence of token i (cu[b] <= i < cu[b + 1]), or -1.
-__device__ __forceinline__ int seq_of(const ExtendParams& p, int i) {
-  if (!p.cu) return i;
-  int lo = 0, hi = p.batch;  // the last b with cu[b] <= i
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu + mid) <= i) lo = mid; else hi = mid;
-  }
-  return i >= __ldg(p.cu + lo) && i < __ldg(p.cu + lo + 1) ? lo : -1;
+__device__ __forceinline__ int seq_of(const ExtendParams& p, int i, int& lo, int& hi) {
+  return seq_of(p.cu, p.batch, p.total, i, lo, hi);
 }
 
 // Pool row of position pos of sequence b, or -1.
@@ -86,8 +67,9 @@ __device__ __forceinline__ bool run_fits(const ExtendParams& p, int b, int count
 
 // Advances the counters of all sequences, once every write of the step has
 // landed: a thread per sequence whose run is short, a warp per one whose run is
-// not (`threads` threads, whole warps).
-__device__ __forceinline__ void extend_commit(const ExtendParams& p, int t, int threads) {
+// not (`threads` threads, whole warps).  sorted: no offset descends.
+__device__ __forceinline__ void extend_commit(const ExtendParams& p, int t, int threads,
+                                              bool sorted) {
   constexpr int SHORT = 128;  // at most three pages
   auto advance = [&](int b, int count, bool ok) {
     if (!ok) {
@@ -101,9 +83,13 @@ __device__ __forceinline__ void extend_commit(const ExtendParams& p, int t, int 
       p.swa_len[b] = spos < CSA2_W ? spos : CSA2_W;
     }
   };
+  auto run_of = [&](int b, int& lo, int& hi) {
+    return run_pair(p.cu, p.total, b, lo, hi) &&
+           (sorted || run_clear(p.cu, p.batch, b, lo, hi));
+  };
   for (int b = t; b < p.batch; b += threads) {
     int lo, hi;
-    const bool order = run_of(p, b, lo, hi);
+    const bool order = run_of(b, lo, hi);
     if (!order) {
       advance(b, 0, false);
     } else if (hi - lo <= SHORT) {
@@ -113,7 +99,7 @@ __device__ __forceinline__ void extend_commit(const ExtendParams& p, int t, int 
   if (p.total <= SHORT) return;
   for (int b = t >> 5; b < p.batch; b += threads >> 5) {
     int lo, hi;
-    if (!run_of(p, b, lo, hi) || hi - lo <= SHORT) continue;
+    if (!run_of(b, lo, hi) || hi - lo <= SHORT) continue;
     const bool ok = __all_sync(0xffffffffu, run_fits(p, b, hi - lo, t & 31, 32));
     if ((t & 31) == 0) advance(b, hi - lo, ok);
   }
@@ -134,7 +120,14 @@ __device__ __forceinline__ void extend_arrive(const ExtendParams& p) {
   }
   __syncthreads();
   if (!last) return;
-  extend_commit(p, threadIdx.x, blockDim.x);
+  bool rise = true;
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+    int lo, hi;
+    run_pair(p.cu, p.total, b, lo, hi);
+    rise = rise && lo <= hi;
+  }
+  const bool sorted = __syncthreads_and(rise);
+  extend_commit(p, threadIdx.x, blockDim.x, sorted);
 }
 
 // Eight channels of one window entry: rotated, E4M3, into its ring slot.
@@ -165,11 +158,10 @@ __device__ __forceinline__ void extend_token(const ExtendParams& p) {
   const int t = threadIdx.x, tok = blockIdx.x;
   const bool main_part = p.x != nullptr && blockIdx.y == 0;
 
-  const int b = seq_of(p, tok);
-  if (b < 0) return;  // behind the last run (extend_commit records bad offsets)
   int lo, hi;
-  const bool in_order = run_of(p, b, lo, hi);
-  if (!__syncthreads_and(in_order && run_fits(p, b, hi - lo, t, EX_NT))) return;
+  const int b = seq_of(p, tok, lo, hi);
+  if (b < 0) return;  // no run's token (extend_commit records bad offsets)
+  if (!__syncthreads_and(run_fits(p, b, hi - lo, t, EX_NT))) return;
 
   if (main_part) {
     const int64_t pos = (int64_t)p.n_rows[b] + (tok - lo);
@@ -321,9 +313,9 @@ __device__ __forceinline__ void et_places(const ExtendParams& p, EtGroup& g, int
   if (t < p.tile && tok < p.total) {
     const char* x = reinterpret_cast<const char*>(p.x + (int64_t)tok * CSA2_D);
     for (int i = 0; i < CSA2_D * 2; i += 128) prefetch_l2(x + i);
-    seq = seq_of(p, tok);
     int lo, hi;
-    if (seq >= 0 && run_of(p, seq, lo, hi)) {
+    seq = seq_of(p, tok, lo, hi);
+    if (seq >= 0) {
       const int64_t at = (int64_t)p.n_rows[seq] + (tok - lo);
       if (at >= 0) row = extend_row(p, seq, at);
       pos = p.pos ? __ldg(p.pos + tok) : (int)at;
@@ -349,7 +341,9 @@ __device__ __forceinline__ void et_check(const ExtendParams& p, EtGroup& g, int 
   const int tok0 = tile * p.tile, seq_hi = g.seq_hi;
   for (int b = g.seq_lo + warp; b <= seq_hi; b += ET_GT / 32) {
     int lo, hi;
-    if (!run_of(p, b, lo, hi) || lo == hi) continue;
+    if (!run_pair(p.cu, p.total, b, lo, hi) || lo == hi) continue;
+    if (!__all_sync(0xffffffffu, run_clear_lane(p.cu, p.batch, b, lane, lo, hi)))
+      continue;  // (no token has its row)
     if (!__all_sync(0xffffffffu, run_fits(p, b, hi - lo, lane, 32)))
       for (int k = max(lo - tok0, 0) + lane; k < min(hi - tok0, p.tile); k += 32)
         g.row[buf][k] = -1;
@@ -560,8 +554,10 @@ constexpr int EW_TOK = 16;
 __device__ __forceinline__ void extend_window(const ExtendParams& p) {
   const int t = threadIdx.x, b = blockIdx.x, l = blockIdx.y, ch = t & 63;
   int lo, hi;
-  if (!run_of(p, b, lo, hi) || hi - (int)blockIdx.z * EW_TOK <= lo) return;
-  if (!__syncthreads_and(run_fits(p, b, hi - lo, t, EX_NT))) return;
+  if (!run_pair(p.cu, p.total, b, lo, hi) || hi - (int)blockIdx.z * EW_TOK <= lo) return;
+  if (!__syncthreads_and(run_clear_lane(p.cu, p.batch, b, t, lo, hi) &&
+                         run_fits(p, b, hi - lo, t, EX_NT)))
+    return;
   const int spos0 = p.swa_pos[b];
   const int end = max(lo, hi - CSA2_W);
   for (int last = hi - blockIdx.z * EW_TOK; last > end; last -= gridDim.z * EW_TOK)
@@ -569,7 +565,7 @@ __device__ __forceinline__ void extend_window(const ExtendParams& p) {
       window_row(p, b, l, tok, spos0 + (tok - lo), ch);
 }
 
-__global__ void __launch_bounds__(EX_NT) extend_window_kernel(const ExtendParams p) {
+__global__ void __launch_bounds__(EX_NT, 4) extend_window_kernel(const ExtendParams p) {
   pdl_launch_dependents();
   pdl_wait();
   extend_window(p);
@@ -580,7 +576,7 @@ __global__ void __launch_bounds__(EX_NT) extend_window_kernel(const ExtendParams
 __global__ void __launch_bounds__(EX_NT) extend_commit_kernel(const ExtendParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  extend_commit(p, blockIdx.x * EX_NT + threadIdx.x, gridDim.x * EX_NT);
+  extend_commit(p, blockIdx.x * EX_NT + threadIdx.x, gridDim.x * EX_NT, false);
 }
 
 cudaError_t launch_extend(const ExtendParams& params, cudaStream_t st) {

@@ -441,7 +441,9 @@ csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32
  * A sequence whose run does not fit (a position beyond its capacity or on an
  * unmapped page, a negative counter, token offsets out of order or beyond
  * total) is left unchanged as a whole, rows, windows and counters, and
- * CSA2_ERR_DEVICE_CHECK is recorded.  ws: at least CSA2_WS_HEADER bytes.
+ * CSA2_ERR_DEVICE_CHECK is recorded.  Where the offsets descend, sequences
+ * beside the descent may be among those left: no token is appended to two, and
+ * none is extended by a part of its run.  ws: at least CSA2_WS_HEADER bytes.
  * ws must have been initialised once (csa2_workspace_init).  One to three
  * launches; asynchronous on stream.
  */
