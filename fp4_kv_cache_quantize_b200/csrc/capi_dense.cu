@@ -91,14 +91,14 @@ csa2_status prefix_params(const csa2_prefix_desc* d, PrefixParams& p) {
   p.swa = d->swa;
   p.swa_len = d->swa_len;
   p.swa_rows = CSA2_W + nq - 1;
-  p.scale_log2 = d->sm_scale * 1.4426950408889634f;
+  p.scale_log2 = d->sm_scale * (1.4426950408889634f / 256);
   p.out = d->out;
   p.grid = prefix_grid(p, num_sms());
   return CSA2_OK;
 }
 
 size_t prefix_ws_bytes(const PrefixParams& p) {
-  return CSA2_WS_HEADER + prefix_partial_rows(p) * (CSA2_D + 2) * sizeof(float) +
+  return CSA2_WS_HEADER + prefix_partial_rows(p) * (CSA2_D + 3) * sizeof(float) +
          prefix_image_tiles(p) * (PREFIX_IMAGE + 64);
 }
 
@@ -244,7 +244,8 @@ csa2_status csa2_prefix_attn(const csa2_prefix_desc* d, void* ws, size_t ws_byte
   p.status = static_cast<uint32_t*>(ws);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + CSA2_WS_HEADER);
   p.part_ml = p.part_o + rows * CSA2_D;
-  p.image = reinterpret_cast<uint8_t*>(p.part_ml + rows * 2);
+  p.part_scl = p.part_ml + rows * 2;
+  p.image = reinterpret_cast<uint8_t*>(p.part_scl + rows);
   p.image_key = p.image + prefix_image_tiles(p) * PREFIX_IMAGE;
   CSA2_CUDA(launch_prefix_attn(p, (cudaStream_t)stream));
   trace_mark("end", (cudaStream_t)stream);

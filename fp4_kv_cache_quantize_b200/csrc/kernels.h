@@ -225,10 +225,11 @@ struct PrefixParams {
   const uint8_t* swa;       // NULL: no window
   const int32_t* swa_len;
   int32_t swa_rows;         // 128 + nq - 1
-  float scale_log2;
+  float scale_log2;         // sm_scale log2(e) / 256
   uint16_t* out;
   float* part_o;    // partials of the shared tiles, then of the own tiles
-  float* part_ml;   // (max, sum) per row, laid out alike
+  float* part_ml;   // (reference, sum) per row, laid out alike
+  float* part_scl;  // what turns accumulators into logits, per row
   uint8_t* image;   // the prefix's tiles in fp16, as the products read them (if the plan has them)
   uint8_t* image_key;  // per key of them: missing (1), holds a NaN (2)
   int32_t grid;     // CTAs that the work is cut for

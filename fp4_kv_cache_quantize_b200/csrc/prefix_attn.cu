@@ -8,12 +8,15 @@
 // in tensor memory.  E2M1 x E4M3 products and E4M3 window values are exact in
 // fp16; a query head is scaled by a power of two into fp16's range.
 //
-// Softmax in one pass: with a reference m per row, p_j = 2^(s_j - m + 7),
-// O += p_j v_j, l += p_j.  m only has to be near the maximum: it is raised (and
-// O, l scaled) when some s_j exceeds it by 8, so p <= 2^15 fits fp16, and the
-// +7 keeps p to 2^-31 of the row's largest before it is lost: a million keys
-// lose at most 2^-12 of the sum together.  (fp16 rounds each p by 2^-11 of
-// itself where bf16 would by 2^-8; l sums them unrounded, in fp32.)
+// Softmax in one pass: with a reference m per row, p_j = 2^(c (a_j - m) + 7),
+// O += p_j v_j, l += p_j, where a_j are the products' accumulators and c >= 0 the
+// row's scale (a negative sm_scale turns the queries' signs instead).  m only has to
+// be near the maximum: it is raised (and O, l scaled) when some c a_j exceeds c m by
+// 8, so p <= 2^15 fits fp16, and the +7 keeps p to 2^-31 of the row's largest before
+// it is lost: a million keys lose at most 2^-12 of the sum together.  (fp16 rounds
+// each p by 2^-11 of itself where bf16 would by 2^-8; l sums them unrounded, in
+// fp32.)  m is one of the a_j, not a logit: c m rounded to fp32 would be off by more
+// than the 8 from 2^28 on, and no logit has to fit fp32 this way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -63,7 +66,12 @@ constexpr int PA_QKB = PA_ROWS * 128;  // one 64-channel chunk of the queries
 constexpr uint32_t PA_S_COL = 256;     // TMEM: O^T in columns [0, 256), two S^T behind
 constexpr uint32_t PA_TMEM_COLS = 512;
 constexpr float PA_SHIFT = 7.0f, PA_SLACK = 8.0f;
-constexpr float PA_NONE = -1e30f;  // reference of a row that has met no key
+// Reference of a row that has met no key.  The first one raises it, except where c is
+// so small (2^-125) that all its p are 2^7 to the last bit.
+constexpr float PA_NONE = -3.402823466e38f;
+constexpr float PA_MOST = 3.402823466e38f;
+// The scale of 1 / 256 that keeps sm_scale log2(e) finite until a row's is made of it.
+constexpr float PA_PRE_SCALE = 256.0f;
 
 // mbar_wait that sleeps until the phase completes, in naps of up to 20 us: the
 // waits' polling otherwise takes issue slots from the warps that work.
@@ -109,7 +117,7 @@ struct PaSmem {
   alignas(1024) uint8_t tile[2][8 * PA_KB];
   alignas(1024) uint8_t q[8 * PA_QKB];        // Q': chunk kb, 64 rows of 128 B
   alignas(1024) uint8_t p[2][PA_KEYS * 128];  // P: [key][64 query rows] fp16
-  alignas(16) float scl[PA_ROWS];             // logit = acc * scl (log2 units)
+  alignas(16) float scl[PA_ROWS];             // logit = acc * scl (log2 units), >= 0
   alignas(16) float fac[PA_ROWS];             // what a raised reference scales O by
   alignas(16) int lo[2][PA_ROWS], hi[2][PA_ROWS];  // cache, window: visible keys [lo, hi)
   int lo_max[2], hi_min[2];                   // keys [lo_max, hi_min) are visible to all rows
@@ -321,6 +329,20 @@ __device__ __forceinline__ uint32_t pa_idesc(int n, bool pv) {
          ((uint32_t)((pv ? 128 : PA_KEYS) >> 4) << 24);
 }
 
+// (a - m) scl + PA_SHIFT of two rows, as packed pairs: as many instructions as one
+// product and sum each (unpacked, 64 x 1 queries over 128K rows 399 us instead of 393).
+__device__ __forceinline__ float2 pa_exponents(float2 a, float m0, float m1, float s0, float s1) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, m, s, h;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+      "mov.b64 h, {%8, %8};\n\t"
+      "add.rn.f32x2 a, a, m;\n\tfma.rn.f32x2 a, a, s, h;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(-m0), "f"(-m1), "f"(s0), "f"(s1), "f"(PA_SHIFT));
+  return y;
+}
+
 // The run that begins at `tile`: the segment of that tile as far as this CTA's
 // share [.., tile_end) goes.
 __device__ __forceinline__ PaRun pa_next_run(const PrefixParams& p, const PaPlan& pl,
@@ -413,9 +435,15 @@ __device__ __forceinline__ void pa_queries(const PrefixParams& p, const PaRun& r
       mx = __reduce_max_sync(0xffffffffu, mx);
       const int e = q_pow2_exponent(mx);
       const int e1 = e / 2, e2 = e - e1;
-      const float f = pow2i(e1), f2 = pow2i(e2);
-      // (where 2^-e leaves fp32's range the logits are below 2^-80 anyway)
-      if (lane == 0) s.scl[h] = p.scale_log2 * PA_TILE_SCALE * pow2i(-e1) * pow2i(-e2);
+      const float f = p.scale_log2 < 0.0f ? -pow2i(e1) : pow2i(e1), f2 = pow2i(e2);
+      // Below fp32's range the logits are below 2^-80 anyway.  Above it only the largest
+      // counts, with PA_MOST too: two sums that differ do so by 2^-41 or more (Q' has
+      // 2^-24, tiles 2^-17 for their last place).  A head that is not finite gives NaN.
+      if (lane == 0)
+        s.scl[h] = mx >= 0x7F80u
+                       ? __int_as_float(0x7FC00000)
+                       : fminf(fabsf(p.scale_log2) * pow2i(-e1) * pow2i(-e2) *
+                                   (PA_PRE_SCALE * PA_TILE_SCALE), PA_MOST);
 #pragma unroll
       for (int k = 0; k < 2; k++) {
         const uint32_t w[4] = {v[u][k].x, v[u][k].y, v[u][k].z, v[u][k].w};
@@ -754,16 +782,19 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         __syncwarp();
         tc_fence_after();
         if (active) {
-          // x[4 n + 2 k + e]: key k0 + 8 k, row c0 + 8 n + e: the logit less f times
-          // the row's reference
-          auto logits = [&](float f, float(&x)[2 * PA_COLS]) {
+          // x[4 n + 2 k + e]: key k0 + 8 k, row c0 + 8 n + e: the exponent of its p, or
+          // its accumulator
+          auto logits = [&](bool sums, float(&x)[2 * PA_COLS]) {
             uint32_t acc[2 * PA_COLS];
             tmem_ld_16x256b(tmem + lane_base + PA_S_COL + PA_ROWS * (i & 1) + PA_PART * part, acc);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 2 * PA_COLS; j++) {
-              const int c = 2 * (j >> 2) + (j & 1);
-              x[j] = fmaf(__uint_as_float(acc[j]), scl[c], f * m[c]);
+            for (int j = 0; j < 2 * PA_COLS; j += 2) {
+              const int c = 2 * (j >> 2);
+              const float2 a = make_float2(__uint_as_float(acc[j]), __uint_as_float(acc[j + 1]));
+              const float2 y = sums ? a : pa_exponents(a, m[c], m[c + 1], scl[c], scl[c + 1]);
+              x[j] = y.x;
+              x[j + 1] = y.y;
             }
             if (!plain) {
 #pragma unroll
@@ -776,14 +807,14 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             }
           };
           float x[2 * PA_COLS];
-          logits(-1.0f, x);
+          logits(false, x);
           float over = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 2 * PA_COLS; j += 2) over = fmaxf(over, fmaxf(x[j], x[j + 1]));
           if (bar_or_128(1 + part, over > PA_SHIFT + PA_SLACK)) {
             // some logit is far above its reference: raise the references to the
             // rows' maxima and scale what was summed
-            logits(0.0f, x);
+            logits(true, x);
 #pragma unroll
             for (int j = 0; j < PA_COLS; j++) {
               float mx = fmaxf(x[4 * (j >> 1) + (j & 1)], x[4 * (j >> 1) + 2 + (j & 1)]);
@@ -797,7 +828,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
             for (int j = 0; j < PA_COLS; j++) {
               const int c = c0 + 8 * (j >> 1) + (j & 1);
               const float mx = fmaxf(fmaxf(s.red[0][c], s.red[1][c]), fmaxf(s.red[2][c], s.red[3][c]));
-              const float top = fmaxf(m[j], mx - PA_SHIFT), f = ex2(m[j] - top);
+              const float top = fmaxf(m[j], mx), f = ex2((m[j] - top) * scl[j]);
               m[j] = top;
               l[j] *= f;
               if (quad == 0 && lane < 4) s.fac[c] = f;
@@ -822,7 +853,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
               }
               tmem_st_wait();
             }
-            logits(-1.0f, x);
+            logits(false, x);
           }
           uint8_t* dst = s.p[i & 1] + k0 * 128 + 4 * (lane & 3);
 #pragma unroll
@@ -861,6 +892,7 @@ __global__ void __launch_bounds__(PA_NT, 1) prefix_attn_kernel(const PrefixParam
         bar_or_128(1 + part, false);
         const int c = PA_PART * part + lane;
         if (quad == 0 && lane < PA_PART && c < run.n_rows) {
+          p.part_scl[run.slot + c] = s.scl[c];
           p.part_ml[2 * (run.slot + c)] = s.fac[c];
           p.part_ml[2 * (run.slot + c) + 1] =
               (s.red[0][c] + s.red[1][c]) + (s.red[2][c] + s.red[3][c]);
@@ -1016,7 +1048,8 @@ __global__ void __launch_bounds__(PI_NT) prefix_image_kernel(const PrefixParams 
   pdl_launch_dependents();
 }
 
-// out = sum_i w_i O_i / sum_i w_i l_i over a row's partials, w_i = 2^(m_i - max m).
+// out = sum_i w_i O_i / sum_i w_i l_i over a row's partials, w_i = 2^(c (m_i - max m)),
+// c the row's scale.
 // All heads of a query share the list of partials.  A CTA takes HEADS heads of one
 // query: all 16 where the queries alone fill the GPU (a CTA's look at the plan
 // costs more than a row's sum), else one, its partials dealt to four groups of 128
@@ -1103,12 +1136,13 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
   }
   // ---- weights: a warp per head (a NaN sum stays one)
   if (warp < HEADS) {
-    float M = -INFINITY;
+    float M = -INFINITY, scl = 0.0f;
     for (int i = lane; i < n; i += 32) {
       float m = -INFINITY;
       if (slot[i] >= 0) {
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot[i] + h0 + warp));
         if (ml.y > 0.0f || ml.y != ml.y) m = ml.x;
+        scl = p.part_scl[slot[i] + h0 + warp];  // (alike in all of them)
       }
       w[i][warp] = m;
       M = fmaxf(M, m);
@@ -1116,7 +1150,7 @@ __global__ void __launch_bounds__(PM_NT) prefix_merge_kernel(const PrefixParams 
     M = warp_max_f32(M);
     float sum = 0.0f;
     for (int i = lane; i < n; i += 32) {
-      const float wt = w[i][warp] == -INFINITY ? 0.0f : exp2f(w[i][warp] - M);
+      const float wt = w[i][warp] == -INFINITY ? 0.0f : exp2f((w[i][warp] - M) * scl);
       w[i][warp] = wt;
       if (slot[i] >= 0 && M != -INFINITY) {
         const float l = p.part_ml[2 * (slot[i] + h0 + warp) + 1];

@@ -488,7 +488,9 @@ csa2_status csa2_cache_extend(const csa2_extend_desc *desc, void *ws, size_t ws_
  *   prefix_rows  in [0, kv.max_rows] (host)
  *   n_query      queries per sequence, in [1, CSA2_MAX_QUERY], their entries
  *                already in the caches; kv.batch * n_query <= 65535
- *   q, out       bf16 [batch][n_query][16][512] (any finite q)
+ *   q, out       bf16 [batch][n_query][16][512]; any finite q and sm_scale, also
+ *                where logits leave fp32's range; a head with a q that is not
+ *                finite gives NaN, the others what they would without it
  *   swa          E4M3 [batch][128 + n_query - 1][512], rows in order, with
  *                swa_len int32 [batch] <= 128 + n_query - 1 (4-byte aligned);
  *                NULL (both): no window
