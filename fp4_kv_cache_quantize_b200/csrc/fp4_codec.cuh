@@ -68,12 +68,12 @@ __device__ __forceinline__ uint32_t fp4_encode8(const float (&f)[8], float group
 }
 
 // Encode one 16-channel group (32 bytes of bf16) in one thread: eight code bytes,
-// the scale's bits in *scale_bits.  The same bits as fp4_encode8 with fewer
-// instructions, by one argument.  What decides is on which side of a midpoint T of
-// the target type a quotient lies, or that it is T.  T and the divisor have so few
-// bits that a quotient which is not T is at least 2^-8 of T away from it, so an
-// approximate product may be snapped to a grid that is coarser than its error,
-// holds every T, and moves nothing by more than 2^-10 of T:
+// the scale's bits in *scale_bits.  The same bits as fp4_encode8, whatever the values,
+// with fewer instructions where they are finite, by one argument.  What decides is on
+// which side of a midpoint T of the target type a quotient lies, or that it is T.  T
+// and the divisor have so few bits that a quotient which is not T is at least 2^-8 of
+// T away from it, so an approximate product may be snapped to a grid that is coarser
+// than its error, holds every T, and moves nothing by more than 2^-10 of T:
 //  * the scale, amax / 6 to E4M3: T has at most 5 significant bits, 6 T as many as 7,
 //    amax 8.  amax times fp32(1/6) is off by 2^-23 and snapped to 11 bits (tf32).
 //  * the codes, x / s to E2M1, T = 1/4 .. 5: x has 8 bits, T s at most 7.
@@ -95,7 +95,16 @@ __device__ __forceinline__ uint2 fp4_encode16(const uint4& a, const uint4& b, ui
   uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
   for (int k = 1; k < 8; k++) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
-  const float t = tf32_rna(__fmul_rn(__uint_as_float(max(m << 16, m & 0xFFFF0000u)), 1.0f / 6.0f));
+  m = max(m << 16, m & 0xFFFF0000u);
+  if (m >= 0x7F800000u) {  // an infinity or NaN, which those instructions treat otherwise
+    float f[8], g[8];
+    unpack_bf16x8(a, f);
+    unpack_bf16x8(b, g);
+    const float amax = fmaxf(amax8(f), amax8(g));
+    const uint32_t first = fp4_encode8(f, amax, scale_bits);
+    return make_uint2(first, fp4_encode8(g, amax, scale_bits));
+  }
+  const float t = tf32_rna(__fmul_rn(__uint_as_float(m), 1.0f / 6.0f));
   const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(sb, __NV_E4M3)));
   *scale_bits = (uint8_t)sb;

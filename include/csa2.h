@@ -438,6 +438,8 @@ csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32
  *   n_layers   0: no windows; x_swa bf16 [n_layers][total][512],
  *              swa E4M3 [n_layers][batch][128][512], swa_pos and swa_len int32
  *              [batch] (4-byte aligned)
+ * Entries may hold infinities and NaN: the rows are as said (the quantiser's own bits),
+ * such a token's key is not finite, and no other token's row, key or window changes.
  * A sequence whose run does not fit (a position beyond its capacity or on an
  * unmapped page, a negative counter, token offsets out of order or beyond
  * total) is left unchanged as a whole, rows, windows and counters, and
