@@ -395,7 +395,8 @@ class CacheExtend:
     x bf16 [total][512] appended to kv's sequences (cu_tokens int32
     [batch + 1]; None: one token each) and x_swa bf16 [L][total][512] to the
     window rings swa E4M3 [L][batch][128][512], rotated by pos int32 [total]
-    (None: the cache position).  See csa2.h."""
+    (None: the cache position).  x None: windows only.  Drafts that may be rejected go
+    in without x_swa, since a ring's overwritten rows are gone.  See csa2.h."""
 
     def __init__(self, kv: KVCache, x=None, w_idx=None, *, cu_tokens=None, pos=None, rope=None,
                  rope_idx=None, rope_swa=None, x_swa=None, swa=None, swa_pos=None, swa_len=None):

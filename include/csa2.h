@@ -408,7 +408,7 @@ csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32
 
 /*
  * Append a run of entries to every sequence, rotated by position on the way:
- * prompt chunks, draft positions, or one entry each.  Tokens
+ * prompt chunks, draft positions (see below), or one entry each.  Tokens
  * cu_tokens[b] .. cu_tokens[b + 1) of x belong to sequence b; token i of its
  * run (count of them) goes to position p = kv.n_rows[b] + i:
  *   codes/scales row of p  <- FP4 of R(x) (as csa2_quantize_fp4 of the bf16
@@ -438,6 +438,14 @@ csa2_status csa2_rope_rows(const csa2_rope *rope, const uint16_t *x, const int32
  *   n_layers   0: no windows; x_swa bf16 [n_layers][total][512],
  *              swa E4M3 [n_layers][batch][128][512], swa_pos and swa_len int32
  *              [batch] (4-byte aligned)
+ * Drafts.  A window entry takes the place of the one 128 before it, which putting
+ * swa_pos back does not bring back, and which the first of several queries still
+ * sees.  So entries that may be rejected are appended with n_layers = 0 (to reject
+ * them put kv.n_rows back: the next run overwrites their rows), and their window
+ * entries, with x NULL and pos given, into scratch rings whose swa_pos is 0.  There
+ * they lie in order: behind the newest 127 rows of the ring they make the window of
+ * csa2_prefix_attn and csa2_layer_group with n_query > 1 (128 + n_query - 1 rows).
+ * Those accepted then go to the rings by a call with x NULL.
  * Entries may hold infinities and NaN: the rows are as said (the quantiser's own bits),
  * such a token's key is not finite, and no other token's row, key or window changes.
  * A sequence whose run does not fit (a position beyond its capacity or on an
