@@ -39,12 +39,21 @@ __host__ __device__ __forceinline__ bool run_pair(const int32_t* cu, int total, 
 // offset of the batch descends they always do.)
 __host__ __device__ __forceinline__ bool run_clear(const int32_t* cu, int batch, int b, int lo,
                                                    int hi) {
+  constexpr int STEPS = 5;  // the way depends on b alone: so many loads together
   bool ok = true;
 #pragma unroll 1
   for (int l = 0, z = cu ? batch : 1; z - l > 1;) {
-    const int mid = (l + z) >> 1, c = run_offset(cu, mid);
-    ok = ok && (mid <= b ? c <= lo : c >= hi);
-    if (mid <= b) l = mid; else z = mid;
+    int c[STEPS];
+    bool right[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; k++) {
+      const int mid = (l + z) >> 1;  // (at the way's end: b itself)
+      c[k] = run_offset(cu, mid);
+      right[k] = mid <= b;
+      if (right[k]) l = mid; else z = mid;
+    }
+#pragma unroll
+    for (int k = 0; k < STEPS; k++) ok = ok && (right[k] ? c[k] <= lo : c[k] >= hi);
   }
   return ok;
 }
@@ -59,7 +68,7 @@ __host__ __device__ __forceinline__ bool run_clear_lane(const int32_t* cu, int b
     if (mid <= b) l = mid; else z = mid;
     mid = (l + z) >> 1;
   }
-  const int c = run_offset(cu, mid);  // (at the way's end: offset b itself)
+  const int c = run_offset(cu, mid);
   return mid <= b ? c <= lo : c >= hi;
 }
 
