@@ -16,14 +16,13 @@ namespace csa2 {
 constexpr int EX_NT = 256;
 constexpr int EX_LAYERS_PER_CTA = EX_NT / 64;
 constexpr int EX_COMMIT_BATCH = 512;  // sequences whose counters the last CTA advances
-// Tokens up to which each has CTAs of its own.  Both ways, without window layers:
-// 256 tokens 12 us (tiles: 17), 512 17 (18), 1,024 25 (16); with 20 layers 512 24
-// (26), 1,024 36 (26).  Runs of one or two tokens never fill a tile's places and
-// windows: 1,024 sequences x 20 layers 63 us (tiles: 102).
+// Tokens up to which each has CTAs of its own.  Both ways in a graph, one run without
+// window layers: 256 tokens 6.8 us (tiles: 10.5), 512 11.3 (10.5), 1,024 15.7 (10.4);
+// with 20 layers 512 15.8 (15.9), 1,024 23 (16).  Runs of one or two tokens never fill a
+// tile's places and windows: 1,024 sequences x 20 layers 37 us (tiles: 100).
 constexpr int EX_FEW = 512;
-// CTAs per SM up to which a token's layers are spread (64 sequences x 20 layers 15 us,
-// 512 43; four layers to a CTA always: 16, 65; with 2 a batch of 16 takes 15 instead
-// of 12).
+// CTAs per SM up to which a token's layers are spread (512 sequences x 20 layers 32 us,
+// 1,024 37; four layers to a CTA always: 46, 57; batches of 64 and fewer alike).
 constexpr int EX_ROOM = 4;
 
 __device__ __forceinline__ int seq_of(const ExtendParams& p, int i, int& lo, int& hi) {
@@ -112,21 +111,21 @@ __device__ __forceinline__ void extend_arrive(const ExtendParams& p) {
   __shared__ int last;
   if (!p.commit) return;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  bool rise = true;  // the other warps look at the offsets while the first one counts
+  if (threadIdx.x >= 32) {
+    for (int b = threadIdx.x - 32; b < p.batch; b += blockDim.x - 32) {
+      int lo, hi;
+      run_pair(p.cu, p.total, b, lo, hi);
+      rise = rise && lo <= hi;
+    }
+  } else if (threadIdx.x == 0) {
     __threadfence();
     const uint32_t n = gridDim.x * gridDim.y * gridDim.z;
     last = atomicAdd(p.status + CSA2_WS_ARRIVE_WORD, 1u) == n - 1;
     if (last) p.status[CSA2_WS_ARRIVE_WORD] = 0u;
   }
-  __syncthreads();
-  if (!last) return;
-  bool rise = true;
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-    int lo, hi;
-    run_pair(p.cu, p.total, b, lo, hi);
-    rise = rise && lo <= hi;
-  }
   const bool sorted = __syncthreads_and(rise);
+  if (!last) return;
   extend_commit(p, threadIdx.x, blockDim.x, sorted);
 }
 
@@ -249,12 +248,13 @@ __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams 
 // in loops short enough to stay in the instruction cache.
 //
 // What bounds it: memory allows 1,440 bytes a token at its rate, 32K tokens in
-// 7.2 us; they take 31.  20,000 of the 57,000 cycles are issue slots (some 20
-// instructions a value: packing, fp64 rotation), 10,000 the first tiles' way from
-// memory, and the rest the dependent phases of a tile (rows, packing, turning,
-// keys).  Two groups of 64 tokens took 33, tiles of 16 tokens 42, shares of the
-// packing handed out to warps one by one 35.  With few tokens the tiles are
-// shorter (16), so that every SM has some.
+// 7.2 us; they take 27 in a graph (31 cold).  19,000 of the 59,000 cycles are issue
+// slots (some 20 instructions a value: packing, fp64 rotation), 10,000 the first tiles'
+// way from memory, and the rest the dependent phases of a tile (rows, packing, turning,
+// keys).  Two groups of 64 tokens took 2 us more, tiles of 16 tokens 11, shares of the
+// packing handed out to warps one by one 4.  With few tokens the tiles are shorter (16),
+// so that every SM has some.  A paged run costs more the longer it is, since et_check
+// looks at all of its pages for every tile: 32K tokens 40 us, 128K 233 (contiguous: 83).
 constexpr int ET_GROUPS = 4;
 constexpr int ET_GT = 256;                              // threads of a group
 constexpr int ET_NT = ET_GROUPS * ET_GT;

@@ -90,19 +90,27 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A group with an infinity or NaN, which those instructions treat otherwise: rare, and
+// kept out of the loops that pack the others.
+static __device__ __noinline__ uint3 fp4_encode16_any(uint4 a, uint4 b) {
+  float f[8], g[8];
+  unpack_bf16x8(a, f);
+  unpack_bf16x8(b, g);
+  const float amax = fmaxf(amax8(f), amax8(g));
+  uint8_t sb;
+  const uint32_t first = fp4_encode8(f, amax, &sb);
+  return make_uint3(first, fp4_encode8(g, amax, &sb), sb);
+}
 __device__ __forceinline__ uint2 fp4_encode16(const uint4& a, const uint4& b, uint8_t* scale_bits) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
   for (int k = 1; k < 8; k++) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
   m = max(m << 16, m & 0xFFFF0000u);
-  if (m >= 0x7F800000u) {  // an infinity or NaN, which those instructions treat otherwise
-    float f[8], g[8];
-    unpack_bf16x8(a, f);
-    unpack_bf16x8(b, g);
-    const float amax = fmaxf(amax8(f), amax8(g));
-    const uint32_t first = fp4_encode8(f, amax, scale_bits);
-    return make_uint2(first, fp4_encode8(g, amax, scale_bits));
+  if (m >= 0x7F800000u) {
+    const uint3 r = fp4_encode16_any(a, b);
+    *scale_bits = (uint8_t)r.z;
+    return make_uint2(r.x, r.y);
   }
   const float t = tf32_rna(__fmul_rn(__uint_as_float(m), 1.0f / 6.0f));
   const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);

@@ -8,8 +8,9 @@
 // the heads' loads on their way together.  8,192 rows x 16 heads, 64 of 512 channels in
 // place (33.5 MB): 14.4 us with the 5 of an empty launch (one head at a time 18.5);
 // 8,000 x 16 heads into another buffer (262 MB) 55 us, 4.7 TB/s (one head: 103, two: 69).
-// HALVES holds 16 channels a head and twice the angles: two heads, 14 to 16 us (four
-// heads spill registers: 18).
+// HALVES holds 16 channels a head and twice the angles: two heads, 14 to 16 us, which
+// still spill 72 bytes of the 64 registers that four CTAs an SM leave (four heads spill
+// 264 and take 18).
 #include "csa2_internal.cuh"
 #include "rope.cuh"
 
