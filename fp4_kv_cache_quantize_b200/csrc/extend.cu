@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(EX_NT) extend_token_kernel(const ExtendParams 
 // in loops short enough to stay in the instruction cache.
 //
 // What bounds it: memory allows 1,440 bytes a token at its rate, 32K tokens in
-// 7.2 us; they take 27 in a graph (31 cold).  19,000 of the 59,000 cycles are issue
+// 7.2 us; they take 27 in a graph (31 cold).  20,000 of the 57,000 cycles are issue
 // slots (some 20 instructions a value: packing, fp64 rotation), 10,000 the first tiles'
 // way from memory, and the rest the dependent phases of a tile (rows, packing, turning,
 // keys).  Two groups of 64 tokens took 2 us more, tiles of 16 tokens 11, shares of the

@@ -34,10 +34,12 @@ namespace csa2 {
 // 2,200.  With the images there it takes 2,600: the chain of a tile buffer, which is
 // its copy (1,500 from request to first byte, 2,600 to last), S^T, softmax (1,300 with
 // its waits) and O^T, one after another but for the parts; there are two buffers.
-//   128K-row prefix, 64 sequences (1,024 rows): 376 us, 0.74 PFLOP/s; 389 call after
-//   call, when the power limit takes the clock to 1.85 GHz
-//   16K-row prefix, 2 x 256 queries (8,192 rows): 367 us, 0.79 PFLOP/s; 369 likewise
-//   1M-row prefix, 4 sequences (64 rows, no images): 227 us, 1.27 TB/s of cache rows
+// The L2 is not what they wait for: over a 16K-row prefix and 64 sequences it gives 23%
+// of its rate (its busiest slice 26%), 83% of it hits.
+//   128K-row prefix, 64 sequences (1,024 rows): 381 us, 0.73 PFLOP/s; 390 to 400 call
+//   after call, when the power limit takes the clock below 1.85 GHz
+//   16K-row prefix, 2 x 256 queries (8,192 rows): 372 us, 0.77 PFLOP/s, 1.9 GHz
+//   1M-row prefix, 4 sequences (64 rows, no images): 229 us, 1.26 TB/s of cache rows
 //   2K-row prefix, 4 sequences: 17 us, the latencies of one tile a CTA (lengths,
 //   plan, page, rows, products, softmax, partial) and of the merge
 //

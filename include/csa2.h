@@ -522,9 +522,12 @@ typedef struct {
   uint16_t *out;
 } csa2_prefix_desc;
 
-/* Workspace bytes of csa2_prefix_attn; 0 on a bad argument.  Partial results,
- * and, where many queries share a long prefix, its rows in fp16 (1,025 bytes a
- * row), made anew by every call. */
+/* Workspace bytes of csa2_prefix_attn; 0 on a bad argument.  Partial results, 515
+ * floats each: one per query head for its own rows and window and one for each band
+ * of the prefix (with many queries a band is 32K rows or more; at most 16), besides some
+ * per CTA.  8 x 1,024 queries over 128K rows take 1.5 GB, 63 x 1,024 over 1M rows 37 GB:
+ * split such batches.  And, where many queries share a long prefix, its rows in fp16
+ * (1,025 bytes a row), made anew by every call. */
 size_t csa2_prefix_attn_workspace_size(const csa2_prefix_desc *desc);
 csa2_status csa2_prefix_attn(const csa2_prefix_desc *desc, void *ws, size_t ws_bytes,
                              csa2_stream_t stream);
