@@ -505,7 +505,8 @@ csa2_status csa2_cache_extend(const csa2_extend_desc *desc, void *ws, size_t ws_
  *                swa_len int32 [batch] <= 128 + n_query - 1 (4-byte aligned);
  *                NULL (both): no window
  * Rows that the page table maps outside the pool are skipped and recorded as
- * CSA2_ERR_DEVICE_CHECK, and so is a count outside its range (clamped).
+ * CSA2_ERR_DEVICE_CHECK (the prefix's are looked up whether or not a query sees
+ * them), and so is a count outside its range (clamped).
  * Results do not depend on timing: every sum has a fixed order.
  * Two or three launches; asynchronous on stream.
  */
